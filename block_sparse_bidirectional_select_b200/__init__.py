@@ -29,6 +29,18 @@ of B tokens denoised over T steps; q, k, v of the block are [H, B, d]):
     losa_step(q, k, v, q_prev, k_pre, v_pre, state, tau) -> LosaStep
     losa_block(qs, ks, vs, k_pre, v_pre, n_sel, tau) -> LosaBlock (all T steps)
 
+Around block-wise generation (rotary positions with several axes, an 8-bit
+cache with one scale for each 64 tokens and head, attention over it, and dense
+attention with capped or biased scores and document or prefix masks; Hq query
+heads share Hkv key/value heads; inputs may be strided views):
+
+    rope_axes(x, positions, sections)        -> y [H, L, d]
+    cache_alloc(N, Hkv, C, d)                -> Cache8 (k8, v8, k_scale, v_scale)
+    cache_append(cache, k, v, start, count)  -> cache (new tokens written)
+    cache_attn(q, cache, lengths, softcap, slopes) -> (o [N, Hq, B, d], lse)
+    document_ranges(starts, L, prefix)       -> ranges [L, 2]
+    scored_attn(q, k, v, softcap, slopes, ranges)  -> (o [Hq, Lq, d], lse)
+
 q, k, v are [H, L, d] bf16 CUDA tensors (d in {64, 128}); o is [H, L, d] bf16,
 lse [H, L] fp32 natural log; kv_idx [H, nqb, kv_stride] int32 and kv_count
 [H, nqb] int32 hold the per-(head, query block) kept key blocks, ascending.
@@ -53,7 +65,9 @@ __all__ = ["dense_attn", "select_pattern", "block_sparse_attn", "run_steps", "wo
            "entropy_budget", "select_with_head_k", "select_pattern_sharded", "gather_head_entropies",
            "run_steps_sharded",
            "losa_splits", "losa_workspace_bytes", "losa_init", "losa_step", "losa_block", "BlockState",
-           "LosaStep", "LosaBlock"]
+           "LosaStep", "LosaBlock",
+           "rope_axes", "Cache8", "cache_alloc", "cache_append", "cache_attn", "cache_attn_workspace_bytes",
+           "document_ranges", "scored_attn", "scored_attn_workspace_bytes", "CACHE_BLOCK"]
 
 
 def _ptr(t: torch.Tensor | None):
@@ -666,3 +680,275 @@ def run_steps_sharded(q, k, v, T, warmup_frac=0.2, keep=0.1, budget="entropy", r
         raise errors[0]
     check(rc, "sparsed_run_steps_sharded")
     return RunResult(out, lse, list(kinds[:T]), None, kv_idx, kv_count)
+
+
+# ---------------------------------------------------------------- rotary axes, 8-bit cache, modified scores
+
+CACHE_BLOCK = 64  # tokens of a cache that share a scale
+
+
+def _device_of(first, **tensors):
+    """The CUDA device all given tensors (None left out) are on."""
+    dev = first.device
+    if dev.type != "cuda":
+        raise ValueError("tensors must be on a CUDA device")
+    for name, t in tensors.items():
+        if t is not None and t.device != dev:
+            raise ValueError(f"{name} must be on {dev}, got {t.device}")
+    return dev
+
+
+def _check_strided(name, t, dims):
+    """A bf16 tensor of `dims` dimensions whose last one is contiguous."""
+    if not isinstance(t, torch.Tensor) or t.dtype != torch.bfloat16:
+        raise TypeError(f"{name} must be a bfloat16 torch.Tensor")
+    if t.dim() != dims:
+        raise ValueError(f"{name} must have {dims} dimensions, got {tuple(t.shape)}")
+    if t.shape[-1] != 1 and t.stride(-1) != 1:
+        raise ValueError(f"{name}: the last dimension must be contiguous")
+
+
+def _strides(t):
+    """Strides of all dimensions but the last; d for one of size 1, whose stride says nothing."""
+    d = t.shape[-1]
+    return [st if n > 1 else d for st, n in zip(t.stride()[:-1], t.shape)]
+
+
+def _check_flat(name, t, dtype, shape):
+    if t.dtype != dtype or tuple(t.shape) != tuple(shape) or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)}, "
+                         f"got {t.dtype} {tuple(t.shape)}")
+
+
+class _Launch:
+    """The device and stream of one call: makes `dev` current, and yields the
+    stream handle. Tensors handed to `keep` (allocated on the current stream)
+    stay reserved until the work on a stream given by the caller is done."""
+
+    def __init__(self, dev, stream):
+        self.index = dev.index if dev.index is not None else torch.cuda.current_device()
+        self.stream = stream
+        self.guard = None
+
+    def __enter__(self):
+        if self.index != torch.cuda.current_device():
+            self.guard = torch.cuda.device(self.index)
+            self.guard.__enter__()
+        self.handle = (torch.cuda.current_stream(self.index) if self.stream is None else self.stream).cuda_stream
+        return self
+
+    def __exit__(self, *exc):
+        if self.guard is not None:
+            self.guard.__exit__(*exc)
+
+    def keep(self, *tensors):
+        if self.stream is not None:
+            for t in tensors:
+                if t is not None:
+                    t.record_stream(self.stream)
+
+
+def _out_like(name, out, shape, dtype, dev):
+    if out is None:
+        return torch.empty(shape, dtype=dtype, device=dev)
+    _check_flat(name, out, dtype, shape)
+    if out.device != dev:
+        raise ValueError(f"{name} must be on {dev}")
+    return out
+
+
+def rope_axes(x, positions, sections, theta=10000.0, interleaved=False, shared_ladder=False, inverse=False,
+              out=None, stream=None):
+    """Rotary positions with several axes. x [H, L, d] bf16 (any strides, the
+    last dimension contiguous, e.g. heads of a projection's output),
+    positions [n_axes, L] int32, sections: the pairs that turn with each axis.
+    Pair j is elements (j, J + j), J = sum(sections), or (2j, 2j + 1) when
+    interleaved; its frequency is theta^-(i / sections[axis]) for the axis'
+    i-th pair, or theta^-(j / J) with shared_ladder. ``inverse`` turns the
+    other way (the gradient's rotation). Returns y [H, L, d]: contiguous, or
+    ``out`` (any strides; may be x)."""
+    _check_strided("x", x, 3)
+    H, L, d = x.shape
+    sections = tuple(int(n) for n in sections)
+    if not isinstance(positions, torch.Tensor) or positions.dtype != torch.int32 or not positions.is_contiguous() \
+            or tuple(positions.shape) != (len(sections), L):
+        raise ValueError(f"positions must be a contiguous int32 tensor [{len(sections)}, {L}]")
+    dev = _device_of(x, positions=positions, out=out)
+    if out is None:
+        out = torch.empty((H, L, d), dtype=torch.bfloat16, device=dev)
+    else:
+        _check_strided("out", out, 3)
+        if out.shape != x.shape:
+            raise ValueError(f"out must be shaped {tuple(x.shape)}, got {tuple(out.shape)}")
+    pairs = (ctypes.c_int * max(len(sections), 1))(*sections)
+    with _Launch(dev, stream) as at:
+        at.keep(x, positions, out)
+        rc = _lib.load().sparsed_rope_axes(
+            x.data_ptr(), *_strides(x), positions.data_ptr(), len(sections), ctypes.addressof(pairs), H, L, d, theta,
+            int(interleaved), int(shared_ladder), int(inverse), out.data_ptr(), *_strides(out), at.handle)
+    check(rc, "sparsed_rope_axes")
+    return out
+
+
+@dataclass
+class Cache8:
+    """Keys and values of N sequences in 8 bits: value = e4m3 * scale."""
+    k8: torch.Tensor       # [N, Hkv, C, d] float8_e4m3fn
+    v8: torch.Tensor
+    k_scale: torch.Tensor  # [N, Hkv, C / 64] fp32, powers of two
+    v_scale: torch.Tensor
+
+
+def cache_alloc(N: int, H: int, C: int, d: int, device="cuda") -> Cache8:
+    """An empty cache of C tokens (a multiple of CACHE_BLOCK) per sequence."""
+    if C % CACHE_BLOCK != 0:
+        raise ValueError(f"the capacity must be a multiple of {CACHE_BLOCK}, got {C}")
+    k8, v8 = (torch.zeros((N, H, C, d), dtype=torch.float8_e4m3fn, device=device) for _ in range(2))
+    ks, vs = (torch.full((N, H, C // CACHE_BLOCK), 2.0 ** -117, dtype=torch.float32, device=device)
+              for _ in range(2))
+    return Cache8(k8, v8, ks, vs)
+
+
+def _check_cache(cache):
+    shape = cache.k8.shape
+    if len(shape) != 4 or shape[2] % CACHE_BLOCK != 0:
+        raise ValueError(f"the cache must be [N, Hkv, C, d] with C a multiple of {CACHE_BLOCK}, got {tuple(shape)}")
+    N, H, C, d = shape
+    for name, t in (("k8", cache.k8), ("v8", cache.v8)):
+        _check_flat(name, t, torch.float8_e4m3fn, shape)
+    for name, t in (("k_scale", cache.k_scale), ("v_scale", cache.v_scale)):
+        _check_flat(name, t, torch.float32, (N, H, C // CACHE_BLOCK))
+    return N, H, C, d
+
+
+def cache_append(cache: Cache8, k, v, start, count=None, stream=None) -> Cache8:
+    """Write k, v [N, Hkv, B, d] bf16 (any strides, the last dimension
+    contiguous) into the cache: the first count[n] tokens (default: all B) of
+    sequence n at positions start[n] on; start, count [N] int32. Tokens of the
+    cache at or past start + count are no longer valid."""
+    _check_strided("k", k, 4)
+    _check_strided("v", v, 4)
+    N, H, C, d = _check_cache(cache)
+    B = k.shape[2]
+    if k.shape != v.shape or tuple(k.shape) != (N, H, B, d):
+        raise ValueError(f"k and v must be [{N}, {H}, B, {d}], got {tuple(k.shape)} and {tuple(v.shape)}")
+    _check_flat("start", start, torch.int32, (N,))
+    if count is not None:
+        _check_flat("count", count, torch.int32, (N,))
+    dev = _device_of(cache.k8, v8=cache.v8, k_scale=cache.k_scale, v_scale=cache.v_scale, k=k, v=v, start=start,
+                     count=count)
+    with _Launch(dev, stream) as at:
+        at.keep(k, v, start, count)
+        rc = _lib.load().sparsed_cache_append(
+            k.data_ptr(), *_strides(k), v.data_ptr(), *_strides(v), N, H, B, C, d, start.data_ptr(),
+            None if count is None else count.data_ptr(), cache.k8.data_ptr(), cache.v8.data_ptr(),
+            cache.k_scale.data_ptr(), cache.v_scale.data_ptr(), at.handle)
+    check(rc, "sparsed_cache_append")
+    return cache
+
+
+def cache_attn_workspace_bytes(N: int, Hq: int, Hkv: int, B: int, d: int) -> int:
+    n = ctypes.c_size_t()
+    check(_lib.load().sparsed_cache_attn_workspace_bytes(N, Hq, Hkv, B, d, ctypes.byref(n)),
+          "sparsed_cache_attn_workspace_bytes")
+    return n.value
+
+
+def cache_attn(q, cache: Cache8, lengths, scale=None, softcap=0.0, slopes=None, q_start=None, out=None, lse=None,
+               workspace=None, stream=None):
+    """Attention of q [N, Hq, B, d] bf16 (one token or a block per sequence)
+    over the first lengths[n] tokens of each sequence's cache: returns
+    (o [N, Hq, B, d] bf16, lse [N, Hq, B] fp32). ``softcap`` caps the scores
+    by softcap * tanh(x / softcap); ``slopes`` [Hq] fp32 subtracts
+    slopes[h] * |position - key|, with the first query token of sequence n at
+    q_start[n] (default lengths[n] - B: the block is the cache's last B
+    tokens). lengths, q_start: [N] int32 on the device."""
+    _check_strided("q", q, 4)
+    N, Hkv, C, d = _check_cache(cache)
+    Hq, B = q.shape[1], q.shape[2]
+    if q.shape[0] != N or q.shape[3] != d or Hkv == 0 or Hq % Hkv != 0:
+        raise ValueError(f"q {tuple(q.shape)} does not fit a cache of {N} sequences, {Hkv} heads, d={d}")
+    _check_flat("lengths", lengths, torch.int32, (N,))
+    if q_start is not None:
+        _check_flat("q_start", q_start, torch.int32, (N,))
+    if slopes is not None:
+        _check_flat("slopes", slopes, torch.float32, (Hq,))
+    dev = _device_of(q, k8=cache.k8, v8=cache.v8, k_scale=cache.k_scale, v_scale=cache.v_scale, lengths=lengths,
+                     q_start=q_start, slopes=slopes, workspace=workspace)
+    out = _out_like("out", out, (N, Hq, B, d), torch.bfloat16, dev)
+    lse = _out_like("lse", lse, (N, Hq, B), torch.float32, dev)
+    if workspace is None:
+        workspace = torch.empty(cache_attn_workspace_bytes(N, Hq, Hkv, B, d), dtype=torch.uint8, device=dev)
+    with _Launch(dev, stream) as at:
+        at.keep(q, cache.k8, cache.v8, cache.k_scale, cache.v_scale, lengths, q_start, slopes, out, lse, workspace)
+        rc = _lib.load().sparsed_cache_attn(
+            q.data_ptr(), *_strides(q), cache.k8.data_ptr(), cache.v8.data_ptr(),
+            cache.k_scale.data_ptr(), cache.v_scale.data_ptr(), N, Hq, Hkv, B, C, d, lengths.data_ptr(),
+            None if q_start is None else q_start.data_ptr(), default_scale(d) if scale is None else scale, softcap,
+            None if slopes is None else slopes.data_ptr(), out.data_ptr(), lse.data_ptr(), workspace.data_ptr(),
+            workspace.numel(), at.handle)
+    check(rc, "sparsed_cache_attn")
+    return out, lse
+
+
+def document_ranges(starts, L: int, prefix=None, stream=None):
+    """Visible keys of packed documents for scored_attn: ranges [L, 2] int32.
+    starts [n + 1] int32 (device, ascending): document i holds tokens
+    starts[i] .. starts[i + 1] - 1, and a token sees its document; with prefix
+    [n] int32 only the document's first prefix[i] tokens and those up to its
+    own (0: causal). Tokens of no document see nothing."""
+    n = starts.numel() - 1
+    if n < 0:
+        raise ValueError("starts must hold the boundaries of the documents")
+    _check_flat("starts", starts, torch.int32, (n + 1,))
+    if prefix is not None:
+        _check_flat("prefix", prefix, torch.int32, (n,))
+    dev = _device_of(starts, prefix=prefix)
+    ranges = torch.empty((L, 2), dtype=torch.int32, device=dev)
+    with _Launch(dev, stream) as at:
+        at.keep(starts, prefix, ranges)
+        rc = _lib.load().sparsed_document_ranges(starts.data_ptr(), None if prefix is None else prefix.data_ptr(), n,
+                                                 L, ranges.data_ptr(), at.handle)
+    check(rc, "sparsed_document_ranges")
+    return ranges
+
+
+def scored_attn_workspace_bytes(Hq: int, Lq: int) -> int:
+    n = ctypes.c_size_t()
+    check(_lib.load().sparsed_scored_attn_workspace_bytes(Hq, Lq, ctypes.byref(n)),
+          "sparsed_scored_attn_workspace_bytes")
+    return n.value
+
+
+def scored_attn(q, k, v, scale=None, softcap=0.0, slopes=None, ranges=None, q_start=0, out=None, lse=None,
+                workspace=None, stream=None):
+    """Dense attention with modified scores: q [Hq, Lq, d], k, v [Hkv, Lk, d]
+    bf16 (strided views with the last dimension contiguous), returns
+    (o [Hq, Lq, d] bf16, lse [Hq, Lq] fp32). ``softcap`` caps the scores by
+    softcap * tanh(x / softcap); ``slopes`` [Hq] fp32 subtracts
+    slopes[h] * |q_start + r - c|; ``ranges`` [Lq, 2] int32 gives the keys
+    [lo, hi) that every row sees (document_ranges; default: all)."""
+    for name, t in (("q", q), ("k", k), ("v", v)):
+        _check_strided(name, t, 3)
+    Hq, Lq, d = q.shape
+    Hkv, Lk = k.shape[0], k.shape[1]
+    if k.shape != v.shape or k.shape[2] != d or Hkv == 0 or Hq % Hkv != 0:
+        raise ValueError(f"q {tuple(q.shape)}, k {tuple(k.shape)} and v {tuple(v.shape)} do not fit")
+    if slopes is not None:
+        _check_flat("slopes", slopes, torch.float32, (Hq,))
+    if ranges is not None:
+        _check_flat("ranges", ranges, torch.int32, (Lq, 2))
+    dev = _device_of(q, k=k, v=v, slopes=slopes, ranges=ranges, workspace=workspace)
+    out = _out_like("out", out, (Hq, Lq, d), torch.bfloat16, dev)
+    lse = _out_like("lse", lse, (Hq, Lq), torch.float32, dev)
+    if workspace is None:
+        workspace = torch.empty(scored_attn_workspace_bytes(Hq, Lq), dtype=torch.uint8, device=dev)
+    with _Launch(dev, stream) as at:
+        at.keep(q, k, v, slopes, ranges, out, lse, workspace)
+        rc = _lib.load().sparsed_scored_attn(
+            q.data_ptr(), *_strides(q), k.data_ptr(), *_strides(k), v.data_ptr(), *_strides(v), Hq,
+            Hkv, Lq, Lk, d, default_scale(d) if scale is None else scale, softcap,
+            None if slopes is None else slopes.data_ptr(), q_start, None if ranges is None else ranges.data_ptr(),
+            out.data_ptr(), lse.data_ptr(), workspace.data_ptr(), workspace.numel(), at.handle)
+    check(rc, "sparsed_scored_attn")
+    return out, lse

@@ -73,6 +73,16 @@ SIGNATURES = {
                                _P, _P, _P, _P, _P, _P, _SZ, _P]),
     "sparsed_losa_block": (_I, [_P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _F, _I, _I, _I, _F, _I, _P, _P, _P,
                                 _P, _P, _P, _P, _P, _SZ, _P]),
+    "sparsed_rope_axes": (_I, [_P, _SZ, _SZ, _P, _I, _P, _I, _I, _I, _F, _I, _I, _I, _P, _SZ, _SZ, _P]),
+    "sparsed_cache_append": (_I, [_P, _SZ, _SZ, _SZ, _P, _SZ, _SZ, _SZ, _I, _I, _I, _I, _I, _P, _P, _P, _P, _P,
+                                  _P, _P]),
+    "sparsed_cache_attn_workspace_bytes": (_I, [_I, _I, _I, _I, _I, ctypes.POINTER(_SZ)]),
+    "sparsed_cache_attn": (_I, [_P, _SZ, _SZ, _SZ, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _P, _P, _F, _F, _P,
+                                _P, _P, _P, _SZ, _P]),
+    "sparsed_document_ranges": (_I, [_P, _P, _I, _I, _P, _P]),
+    "sparsed_scored_attn_workspace_bytes": (_I, [_I, _I, ctypes.POINTER(_SZ)]),
+    "sparsed_scored_attn": (_I, [_P, _SZ, _SZ, _P, _SZ, _SZ, _P, _SZ, _SZ, _I, _I, _I, _I, _I, _F, _F, _P, _I, _P,
+                                 _P, _P, _P, _SZ, _P]),
 }
 
 _lib = None

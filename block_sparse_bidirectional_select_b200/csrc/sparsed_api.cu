@@ -20,6 +20,9 @@
 #include "select_kernels.cuh"
 #include "column_kernels.cuh"
 #include "losa_kernels.cuh"
+#include "rope_kernels.cuh"
+#include "cache_kernels.cuh"
+#include "score_rows_kernel.cuh"
 
 using namespace sparsed;
 
@@ -1728,3 +1731,5 @@ int sparsed_losa_block(const uint16_t* Qs, const uint16_t* Ks, const uint16_t* V
 }
 
 }  // extern "C"
+
+#include "serve_api.cuh"

@@ -556,6 +556,119 @@ int sparsed_losa_block(const uint16_t* Qs, const uint16_t* Ks, const uint16_t* V
                        uint16_t* Os, float* LSEs, int32_t* actives, int32_t* union_counts,
                        void* workspace, size_t workspace_bytes, void* stream);
 
+/* ---- Around block-wise generation: rotary positions with several axes, an
+ * 8-bit cache of keys and values with the attention that reads it, and dense
+ * attention with modified scores. These entry points take strided inputs, so
+ * that heads can be read where a projection wrote them: a stride is counted in
+ * elements, and the d elements of a head row are contiguous. Outputs are
+ * written whole by every call. */
+
+/* Rotary positions with n_axes axes (for example time, height and width).
+ * X and Y are [H, L, d] bf16 with the given strides; Y may be X with the same
+ * strides, and must not overlap it otherwise. positions is [n_axes, L] int32
+ * (any sign). sections (HOST, [n_axes]) are the pairs that turn with each
+ * axis, in order; their sum J gives 2J <= d turned elements, the rest is
+ * copied. Pair j is elements (j, J + j), or (2j, 2j + 1) when interleaved != 0,
+ * and turns by positions[axis] * theta^-x radians, x = i / sections[axis] for
+ * the i-th pair of its axis, or j / J when shared_ladder != 0:
+ *   a' = a cos - b sin,  b' = b cos + a sin    (fp32, rounded once)
+ * inverse != 0 turns the other way, which is also the gradient's rotation.
+ * Angles are exact to 2^-32 turns plus |position| * 2^-53. d is a multiple of
+ * 8 in 8..512, n_axes <= 8, J <= 128, theta >= 1. Any alignment and strides;
+ * fastest with J and all strides multiples of 8 and 16-byte aligned X, Y. */
+int sparsed_rope_axes(const uint16_t* X, size_t x_stride_h, size_t x_stride_l,
+                      const int32_t* positions, int n_axes, const int* sections,
+                      int H, int L, int d, float theta, int interleaved, int shared_ladder, int inverse,
+                      uint16_t* Y, size_t y_stride_h, size_t y_stride_l, void* stream);
+
+/* Tokens of a cache that share a scale. */
+#define SPARSED_CACHE_BLOCK 64
+
+/* Writes new tokens of N sequences into their caches.
+ * The cache: k8, v8 [N, H, C, d] e4m3 (C a multiple of 64, 16-byte aligned),
+ * k_scale, v_scale [N, H, C / 64] fp32, one power of two 2^e, -117 <= e <= 119,
+ * for each block of 64 tokens and head; a cached value is e4m3 * scale.
+ * K and V are [N, H, B, d] bf16 with the given strides. Sequence n gets the
+ * first count[n] tokens (null: all B; 0 <= count <= B) at positions start[n]
+ * .. start[n] + count[n] - 1 (start, count DEVICE [N] int32), 1 <= B <= C. For
+ * every touched block:
+ *   - e is the smallest exponent with amax <= 448 * 2^e over the block's new
+ *     values (infinities and NaN left out; -117 if all are 0), and at least
+ *     the old exponent if the block also holds tokens before start[n], which
+ *     are then rounded again to the new scale (exact unless they become
+ *     subnormal);
+ *   - new values are rounded to nearest even; beyond +-448 * 2^e (infinities)
+ *     they become that bound, and NaN stays NaN.
+ * Bytes of tokens at or past start + count are left as they are; where their
+ * block's scale changed they no longer mean what they did. A sequence with
+ * start < 0, count outside 0..B or start + count > C is skipped and reported
+ * as SPARSED_ERR_BAD_PATTERN by the next sparsed_check. d in {64, 128}. */
+int sparsed_cache_append(const uint16_t* K, size_t k_stride_n, size_t k_stride_h, size_t k_stride_b,
+                         const uint16_t* V, size_t v_stride_n, size_t v_stride_h, size_t v_stride_b,
+                         int N, int H, int B, int C, int d, const int32_t* start, const int32_t* count,
+                         uint8_t* k8, uint8_t* v8, float* k_scale, float* v_scale, void* stream);
+
+/* Workspace bytes of sparsed_cache_attn for these sizes (independent of the
+ * cache's capacity and the sequences' lengths). */
+int sparsed_cache_attn_workspace_bytes(int N, int Hq, int Hkv, int B, int d, size_t* bytes);
+
+/* Attention of B query tokens of each of N sequences over their 8-bit caches
+ * (one token per sequence, or a block being denoised).
+ * Q is [N, Hq, B, d] bf16 (16-byte aligned, strides multiples of 8); the cache
+ * as sparsed_cache_append's, with Hkv heads, each serving the Hq / Hkv query
+ * heads from h * Hq / Hkv on. Every query token of sequence n sees the keys
+ * 0 .. lengths[n] - 1 (DEVICE [N] int32, clamped to 0..C):
+ *   x   = scale * <q, k_c>
+ *   x   = softcap * tanh(x / softcap)            if softcap > 0
+ *   x   = x - slopes[h] * |q_start[n] + b - c|   if slopes is given ([Hq] fp32)
+ *   O   = sum_c softmax(x)_c v_c   (bf16 [N, Hq, B, d]),  LSE = ln sum_c exp(x)
+ *         (fp32 [N, Hq, B])
+ * q_start (DEVICE [N] int32, null: lengths[n] - B) is the position of a
+ * sequence's first query token. Cached bytes past lengths[n] are never used,
+ * whatever they hold. length 0 gives O = 0 and LSE = -inf. LSE and O merge
+ * with attention over other keys by the two-part LSE identity. softcap >= 0,
+ * scale >= 0. Results do not depend on what else is in the batch up to
+ * rounding, and are the same bits on every call with the same lengths.
+ * workspace: sparsed_cache_attn_workspace_bytes, 256-byte aligned, contents
+ * ignored; one workspace must not serve two calls at the same time. */
+int sparsed_cache_attn(const uint16_t* Q, size_t q_stride_n, size_t q_stride_h, size_t q_stride_b,
+                       const uint8_t* k8, const uint8_t* v8, const float* k_scale, const float* v_scale,
+                       int N, int Hq, int Hkv, int B, int C, int d, const int32_t* lengths,
+                       const int32_t* q_start, float scale, float softcap, const float* slopes,
+                       uint16_t* O, float* LSE, void* workspace, size_t workspace_bytes, void* stream);
+
+/* Visible key ranges of packed documents for sparsed_scored_attn: ranges[r] =
+ * [lo, hi) of token r (DEVICE [L, 2] int32, 8-byte aligned). starts (DEVICE
+ * [n_docs + 1] int32, ascending): document i holds tokens starts[i] ..
+ * starts[i + 1] - 1. Without prefix a token sees its whole document; with
+ * prefix (DEVICE [n_docs] int32) the document's first prefix[i] tokens and
+ * those up to its own (0: causal). Tokens of no document get an empty range. */
+int sparsed_document_ranges(const int32_t* starts, const int32_t* prefix, int n_docs, int L,
+                            int32_t* ranges, void* stream);
+
+/* Workspace bytes of sparsed_scored_attn for these sizes. */
+int sparsed_scored_attn_workspace_bytes(int Hq, int Lq, size_t* bytes);
+
+/* Dense attention with modified scores. Q is [Hq, Lq, d], K and V are
+ * [Hkv, Lk, d] bf16 (16-byte aligned, strides multiples of 8; Hq a multiple of
+ * Hkv, query head h reads kv head h / (Hq / Hkv)). Query row r sees the keys
+ * c of its range ranges[r] = [lo, hi) (DEVICE [Lq, 2] int32, 8-byte aligned,
+ * clamped to 0..Lk, shared by all heads; null: every key), with
+ *   x = scale * <q_r, k_c>
+ *   x = softcap * tanh(x / softcap)         if softcap > 0
+ *   x = x - slopes[h] * |q_start + r - c|   if slopes is given (DEVICE [Hq] fp32)
+ *   O[h,r,:] = sum_c softmax(x)_c v_c  (bf16 [Hq, Lq, d]),
+ *   LSE[h,r] = ln sum_c exp(x)         (fp32 [Hq, Lq])
+ * A row that sees nothing gives O = 0 and LSE = -inf. scale >= 0, softcap >= 0.
+ * workspace: sparsed_scored_attn_workspace_bytes, 256-byte aligned, contents
+ * ignored; one workspace must not serve two calls at the same time. */
+int sparsed_scored_attn(const uint16_t* Q, size_t q_stride_h, size_t q_stride_l,
+                        const uint16_t* K, size_t k_stride_h, size_t k_stride_l,
+                        const uint16_t* V, size_t v_stride_h, size_t v_stride_l,
+                        int Hq, int Hkv, int Lq, int Lk, int d, float scale, float softcap,
+                        const float* slopes, int q_start, const int32_t* ranges,
+                        uint16_t* O, float* LSE, void* workspace, size_t workspace_bytes, void* stream);
+
 #ifdef __cplusplus
 }
 #endif
