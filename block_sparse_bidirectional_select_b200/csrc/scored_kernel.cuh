@@ -1,0 +1,723 @@
+// Dense attention with modified scores for sm_100a: capped (tanh) scores, a
+// distance bias, per-row key ranges (document and prefix masks) and key/value
+// heads shared by several query heads. Two query tiles per CTA.
+//
+//   x = scale * <q_r, k_c>;  x = cap * tanh(x / cap);  x -= slope_h * |q_start + r - c|
+//   O_r = sum over c in [lo_r, hi_r) of softmax(x)_c v_c
+//
+// The pipeline is that of attn_kernel.cuh: pairs of query tiles share the K/V
+// tiles of one ring, each slot has its own S/P and O in TMEM, its softmax
+// warpgroup and its MMA issuer, and PV is issued in two parts. What differs:
+//   * the producer reads the ranges of a pair's rows and walks only the key
+//     tiles between the smallest lo and the largest hi (publishing that span
+//     with the pair); a pair whose rows see nothing has no tiles at all;
+//   * each softmax thread holds one row and its range; a warp masks only tiles
+//     that are not inside the ranges of all its 32 rows;
+//   * the scores are modified in registers between the TMEM load and the
+//     exponentials (below);
+//   * with ranges, warp 11 clears the V rows of a tile that no row of the pair
+//     sees, so that whatever padding holds (0 * NaN) stays out of O. It looks
+//     closer only at tiles that no single row sees whole;
+//   * when the pairs would leave SMs idle, a CTA takes single query tiles.
+//
+// Capped scores. tanh(u) = u * P(u^2) for |u| <= 0.6, P of degree 4 by a
+// minimax fit (absolute error 2e-8; the coefficients are scaled on the host so
+// that the polynomial takes the raw product and gives log2 units). It costs
+// six packed FP32 operations for two scores, two of which replace the scaling
+// of the plain path. A warp whose tile holds a larger score takes
+// 1 - 2 / (1 + e^2u), two MUFU operations, whose absolute error (2^-23) is as
+// good; MUFU is what bounds that path (16 operations a clock and SM, three
+// per score with the softmax's own).
+#pragma once
+
+#include <type_traits>
+
+#include "attn_kernel.cuh"
+
+namespace sparsed {
+
+struct ScoredArgs {
+  int H, group;             // query heads, query heads per kv head
+  int L, Lk;                // query rows, keys
+  int nqb, qpp;             // query tiles of 128 rows per head; tiles per CTA and turn (1 or 2)
+  float scale_log2;         // scale * log2(e), above 0
+  const float* slopes;      // [H] or null
+  int q_start;
+  const int2* ranges;       // [L] or null
+  // capped scores: y = s * P(s^2) in log2 units while |s| <= cap_fast, else
+  // cap_log2 * tanh(s * cap_in)
+  float cap_c[5];
+  float cap_fast, cap_in, cap_log2;
+  float* lse;               // [H, L]
+  uint16_t* o;              // [H, L, D]
+  uint64_t timeout_ns;
+  int* sched;               // as AttnArgs
+};
+
+template <int D>
+struct ScoredCfg {
+  static constexpr int BK = 128;
+  using A = AttnCfg<D, BK>;
+  static constexpr int NST = A::NST;
+  static constexpr int B_VOK = A::NUM_BARS;           // [NST] V tile cleared of unseen rows
+  static constexpr int NUM_BARS = B_VOK + NST;
+  static constexpr int N_WTAKERS = A::N_WTAKERS + 1;  // and warp 11
+  static constexpr int OFF_MISC = A::OFF_BAR + NUM_BARS * 8;  // tmem slot, abort flag, 2 x (pair, first tile, tiles)
+  static constexpr int SMEM_BYTES = OFF_MISC + 32 + 1024;
+  static_assert(SMEM_BYTES <= A::SMEM_LIMIT, "shared memory budget");
+};
+
+// tanh(u) for any u: 1 - 2 / (1 + 2^(2 u log2 e)); saturates to +-1.
+__device__ __forceinline__ float tanh_wide(float u) {
+  const float e = ptx::ex2(u * 2.885390081777926815f);
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.0f + e));
+  return fmaf(-2.0f, r, 1.0f);
+}
+
+__device__ __forceinline__ uint64_t mul_f32x2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+
+// P(s^2) for a pair of raw scores.
+__device__ __forceinline__ uint64_t cap_poly(uint64_t s, const uint64_t (&c)[5]) {
+  const uint64_t w = mul_f32x2(s, s);
+  uint64_t p = ptx::fma_f32x2(c[4], w, c[3]);
+  p = ptx::fma_f32x2(p, w, c[2]);
+  p = ptx::fma_f32x2(p, w, c[1]);
+  return ptx::fma_f32x2(p, w, c[0]);
+}
+
+// s[0..N): bias of N consecutive keys from c0 on added, in log2 units; the
+// keys of a warp's tile are all left of its rows (side -1), all right (+1) or
+// around them (0).
+template <int N>
+__device__ __forceinline__ void add_bias(float (&s)[N], float slope2, int at, int c0, int side) {
+  // |at - c| with c = c0 + e: exact in fp32 up to 2^24
+  const float d0 = static_cast<float>(at - c0);
+  if (side == 0) {
+#pragma unroll
+    for (int e = 0; e < N; ++e) s[e] = fmaf(-slope2, fabsf(d0 - static_cast<float>(e)), s[e]);
+  } else {
+    const float b1 = side < 0 ? slope2 : -slope2;  // per key
+    const float b0 = -slope2 * fabsf(d0);
+    const uint64_t b11 = ptx::f32x2(b1, b1), b00 = ptx::f32x2(b0, b0);
+#pragma unroll
+    for (int e = 0; e < N; e += 2) {
+      const uint64_t t = ptx::fma_f32x2(ptx::f32x2(static_cast<float>(e), static_cast<float>(e + 1)), b11, b00);
+      ptx::f32x2_split(ptx::add_f32x2(ptx::f32x2(s[e], s[e + 1]), t), s[e], s[e + 1]);
+    }
+  }
+}
+
+template <int N>
+__device__ __forceinline__ float row_max(const float (&s)[N]) {
+  float mx0 = s[0], mx1 = s[1], mx2 = s[2], mx3 = s[3];
+#pragma unroll
+  for (int c = 4; c < N; c += 8) {
+    mx0 = ptx::max3(mx0, s[c], s[c + 1]);
+    mx1 = ptx::max3(mx1, s[c + 2], s[c + 3]);
+    if (c + 4 < N) {
+      mx2 = ptx::max3(mx2, s[c + 4], s[c + 5]);
+      mx3 = ptx::max3(mx3, s[c + 6], s[c + 7]);
+    }
+  }
+  return fmaxf(fmaxf(mx0, mx1), fmaxf(mx2, mx3));
+}
+template <int N>
+__device__ __forceinline__ float row_min(const float (&s)[N]) {
+  float m0 = s[0], m1 = s[1];
+#pragma unroll
+  for (int c = 2; c < N; c += 2) {
+    m0 = fminf(m0, s[c]);
+    m1 = fminf(m1, s[c + 1]);
+  }
+  return fminf(m0, m1);
+}
+
+// The exponentials of 32 scores of a row in log2 units: CAPPED takes raw
+// scores through the polynomial on the way.
+template <bool CAPPED>
+__device__ __forceinline__ void scored_exp32(const float* s, uint64_t mul2, uint64_t negm2, const uint64_t (&cap)[5],
+                                             uint32_t (&pk)[16], uint64_t& acc0, uint64_t& acc1) {
+#pragma unroll
+  for (int e = 0; e < 16; ++e) {
+    const uint64_t v = ptx::f32x2(s[2 * e], s[2 * e + 1]);
+    uint64_t arg;
+    if constexpr (CAPPED) arg = ptx::fma_f32x2(v, cap_poly(v, cap), negm2);
+    else arg = ptx::fma_f32x2(v, mul2, negm2);
+    float x0, x1;
+    ptx::f32x2_split(arg, x0, x1);
+    const float p0 = ptx::ex2(x0), p1 = ptx::ex2(x1);
+    if (e & 1) acc1 = ptx::add_f32x2(acc1, ptx::f32x2(p0, p1));
+    else acc0 = ptx::add_f32x2(acc0, ptx::f32x2(p0, p1));
+    pk[e] = ptx::pack_bf16x2(p0, p1);
+  }
+}
+
+struct ScoredPair {
+  int h, q0;
+  bool has1;
+};
+// turn w: head w / nph; its later (under causal masks longer) tiles first
+__device__ __forceinline__ ScoredPair scored_pair(const ScoredArgs& a, int w, int nph) {
+  ScoredPair r;
+  r.h = w / nph;
+  r.q0 = (nph - 1 - (w - r.h * nph)) * a.qpp;
+  r.has1 = a.qpp == 2 && r.q0 + 1 < a.nqb;
+  return r;
+}
+
+// [lo, hi) of row r clamped to the keys; rows past the last see all of them
+// when `outside_all`, else nothing.
+__device__ __forceinline__ int2 scored_range(const ScoredArgs& a, int r, bool outside_all) {
+  int2 v = make_int2(0, a.Lk);
+  if (r >= a.L) return outside_all ? v : make_int2(0, 0);
+  if (a.ranges) {
+    v = a.ranges[r];
+    v.x = max(v.x, 0);
+    v.y = min(v.y, a.Lk);
+  }
+  return v;
+}
+
+template <int D, bool CAP, bool BIAS>
+__global__ void __launch_bounds__(384, 1)
+    scored_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
+                       const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ ScoredArgs a) {
+  using S = ScoredCfg<D>;
+  using C = typename S::A;
+  constexpr int BK = S::BK;
+  constexpr int NST = C::NST;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                             ~static_cast<uintptr_t>(1023));
+  const uint32_t sb = ptx::smem_u32(smem);
+  const int warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31;
+  const int nph = (a.nqb + a.qpp - 1) / a.qpp;
+  const int n_pairs = a.H * nph;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + S::OFF_MISC);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + S::OFF_MISC + 4);
+  // the producer publishes each turn here, double-buffered: pair, first key tile, key tiles
+  volatile int* turn = reinterpret_cast<volatile int*>(smem + S::OFF_MISC + 8);
+  auto bar = [&](int idx) -> uint32_t { return sb + C::OFF_BAR + 8 * idx; };
+
+  // ---- setup
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < 2; ++s) {
+      ptx::mbar_init(bar(C::B_WFULL + s), 1);
+      ptx::mbar_init(bar(C::B_WEMPTY + s), S::N_WTAKERS);
+      ptx::mbar_init(bar(C::B_QFULL + s), 1);
+      ptx::mbar_init(bar(C::B_QEMPTY + s), 1);
+      ptx::mbar_init(bar(C::B_SFULL + s), 1);
+      for (int q = 0; q < C::NPV; ++q)
+        ptx::mbar_init(bar(C::B_PFULL + s * C::NPV + q), 4);  // one arrival per softmax warp of the slot
+      ptx::mbar_init(bar(C::B_PVDONE + s), 1);
+      ptx::mbar_init(bar(C::B_DRAIN + s), 1);
+    }
+    for (int s = 0; s < NST; ++s) {
+      ptx::mbar_init(bar(C::B_FULL + s), 1);
+      ptx::mbar_init(bar(C::B_EMPTY + s), a.ranges ? 3 : 2);  // two commits per tile, and warp 11
+      ptx::mbar_init(bar(S::B_VOK + s), 1);
+    }
+    *abort_flag = 0;
+    ptx::fence_mbar_init();
+  }
+  if (warp == 9) {
+    ptx::tmem_alloc(ptx::smem_u32(tmem_slot), C::TM_ALLOC);
+    ptx::tmem_relinquish();
+  }
+  ptx::tc_fence_before();
+  __syncthreads();
+  ptx::tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+
+  if (warp >= 8) {
+    setmaxnreg_dec_56();
+    const uint32_t leader = ptx::elect_one();
+    auto wait = [&](int idx, int parity) -> bool {
+      return ptx::mbar_wait_warp(bar(idx), parity & 1, abort_flag, a.timeout_ns, kErrTimeout);
+    };
+    if (warp == 8) {
+      // ============================================================ producer
+      if (leader) {
+        ptx::tma_prefetch_desc(&tm_q);
+        ptx::tma_prefetch_desc(&tm_k);
+        ptx::tma_prefetch_desc(&tm_v);
+      }
+      int seq = 0;               // ring tiles issued
+      int qn0 = 0, qn1 = 0;      // Q tiles issued per slot
+      bool ok = true;
+      int hk = 0, h = 0;
+      auto load_tile = [&](const CUtensorMap* tm, int blk) -> bool {
+        const int st = seq % NST;
+        if (seq >= NST && !wait(C::B_EMPTY + st, (seq / NST) - 1)) return false;
+        ptx::mbar_arrive_expect_tx_if(leader, bar(C::B_FULL + st), C::KV_BYTES);
+#pragma unroll
+        for (int c = 0; c < C::DCH; ++c)
+          ptx::tma_load_3d_if(leader, sb + C::OFF_RING + st * C::KV_BYTES + c * C::KV_CHUNK, tm, bar(C::B_FULL + st),
+                              c * 64, blk * BK, hk);
+        ++seq;
+        return true;
+      };
+      auto load_q = [&](int s, int qi) -> bool {
+        const int qn = s ? qn1 : qn0;
+        if (qn > 0 && !wait(C::B_QEMPTY + s, qn - 1)) return false;
+        ptx::mbar_arrive_expect_tx_if(leader, bar(C::B_QFULL + s), C::Q_BYTES);
+#pragma unroll
+        for (int c = 0; c < C::DCH; ++c)
+          ptx::tma_load_3d_if(leader, sb + (s ? C::OFF_Q1 : C::OFF_Q0) + c * C::Q_CHUNK, &tm_q, bar(C::B_QFULL + s),
+                              c * 64, qi * 128, h);
+        if (s) ++qn1;
+        else ++qn0;
+        return true;
+      };
+      int np = 0;  // turns published
+      auto publish = [&](int w, int j0, int nj) -> bool {
+        const int b = np & 1;
+        if (np >= 2 && !wait(C::B_WEMPTY + b, (np >> 1) - 1)) return false;
+        if (leader) {
+          turn[3 * b] = w;
+          turn[3 * b + 1] = j0;
+          turn[3 * b + 2] = nj;
+          ptx::mbar_arrive(bar(C::B_WFULL + b));
+        }
+        __syncwarp();
+        ++np;
+        return true;
+      };
+      int w = blockIdx.x;
+      while (ok) {
+        if (w >= n_pairs) {
+          publish(n_pairs, 0, 0);
+          break;
+        }
+        const ScoredPair pr = scored_pair(a, w, nph);
+        h = pr.h;
+        hk = h / a.group;
+        // the key tiles between the smallest lo and the largest hi of the pair's rows
+        int lo = 0, hi = a.Lk;
+        if (a.ranges) {
+          lo = a.Lk;
+          hi = 0;
+          const int rows = pr.has1 ? 256 : 128;
+          for (int u = lane; u < rows; u += 32) {
+            const int2 v = scored_range(a, pr.q0 * 128 + u, false);
+            if (v.x < v.y) {
+              lo = min(lo, v.x);
+              hi = max(hi, v.y);
+            }
+          }
+          lo = __reduce_min_sync(0xffffffffu, lo);
+          hi = __reduce_max_sync(0xffffffffu, hi);
+        }
+        const int j0 = lo / BK;
+        const int nj = hi > lo ? (hi + BK - 1) / BK - j0 : 0;
+        ok = publish(w, j0, nj);
+        if (!ok) break;
+        // the CTA's next turn: the static stride, or a claim on the counter
+        int w_next = w + static_cast<int>(gridDim.x);
+        if (a.sched) {
+          int claim = 0;
+          if (leader) claim = atomicAdd(a.sched, 1);
+          w_next = static_cast<int>(gridDim.x) + __reduce_max_sync(0xffffffffu, claim);
+        }
+        if (leader && w_next < n_pairs) {
+          const ScoredPair pn = scored_pair(a, w_next, nph);
+#pragma unroll
+          for (int c = 0; c < C::DCH; ++c) {
+            ptx::tma_prefetch_3d(&tm_q, c * 64, pn.q0 * 128, pn.h);
+            if (pn.has1) ptx::tma_prefetch_3d(&tm_q, c * 64, (pn.q0 + 1) * 128, pn.h);
+          }
+        }
+        // in the order the slots consume them: Q0, K_0, Q1, V_0, K_1, V_1, ...
+        for (int j = 0; ok && j < nj; ++j) {
+          if (j == 0) ok = load_q(0, pr.q0);
+          if (ok) ok = load_tile(&tm_k, j0 + j);
+          if (ok && pr.has1 && j == 0) ok = load_q(1, pr.q0 + 1);
+          if (ok) ok = load_tile(&tm_v, j0 + j);
+        }
+        w = w_next;
+      }
+      if (!ok) {
+        // let the copies in flight land before the CTA's shared memory goes away
+        const uint64_t short_ns = a.timeout_ns / 4;
+        volatile int dummy = 0;
+        if (qn0 > 0) ptx::mbar_wait(bar(C::B_QFULL + 0), (qn0 - 1) & 1, &dummy, short_ns, 0);
+        if (qn1 > 0) ptx::mbar_wait(bar(C::B_QFULL + 1), (qn1 - 1) & 1, &dummy, short_ns, 0);
+        for (int u = (seq > NST ? seq - NST : 0); u < seq; ++u)
+          ptx::mbar_wait(bar(C::B_FULL + u % NST), (u / NST) & 1, &dummy, short_ns, 0);
+        __syncwarp();
+      }
+    } else if (warp == 9 || warp == 10) {
+      // ============================================================ MMA issuers (as attn_fwd_kernel)
+      const int s = warp - 9;
+      constexpr uint32_t HI = ptx::sdesc_sw128_hi(1024);
+      const uint32_t q_lo = ptx::sdesc_sw128_lo(sb + (s ? C::OFF_Q1 : C::OFF_Q0), 16);
+      const uint32_t k_lo = ptx::sdesc_sw128_lo(sb + C::OFF_RING, 16);
+      const uint32_t v_lo = ptx::sdesc_sw128_lo(sb + C::OFF_RING, C::KV_CHUNK);
+      const uint32_t s_tmem = tmem + (s ? C::TM_S1 : C::TM_S0);
+      const uint32_t o_tmem = tmem + (s ? C::TM_O1 : C::TM_O0);
+      constexpr int KPP = BK / 16 / C::NPV;  // PV MMAs per part of P
+      int seq = 0;      // ring tiles (same numbering as the producer)
+      int qn = 0;       // Q tiles consumed
+      int tcnt = 0;     // tiles of this slot (PFULL phases)
+      bool ok = true;
+      auto commit = [&](int idx) { ptx::umma_commit_if(leader, bar(idx)); };
+      for (int np = 0; ok; ++np) {
+        if (!wait(C::B_WFULL + (np & 1), np >> 1)) {
+          ok = false;
+          break;
+        }
+        const int w = turn[3 * (np & 1)];
+        const int nj = turn[3 * (np & 1) + 2];
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(bar(C::B_WEMPTY + (np & 1)));
+        if (w >= n_pairs) break;
+        const ScoredPair pr = scored_pair(a, w, nph);
+        const bool mine = s == 0 || pr.has1;
+        const bool sole = !pr.has1;
+        for (int j = 0; j < nj; ++j) {
+          const int sk = seq, sv = seq + 1;
+          seq += 2;
+          if (!mine) continue;
+          if ((j == 0 && !wait(C::B_QFULL + s, qn++)) || !wait(C::B_FULL + sk % NST, sk / NST)) {
+            ok = false;
+            break;
+          }
+          ptx::tc_fence_after();
+#pragma unroll
+          for (int kk = 0; kk < D / 16; ++kk) {
+            constexpr uint32_t QC = C::Q_CHUNK >> 4, KC = C::KV_CHUNK >> 4;
+            const uint32_t ao = (kk >> 2) * QC + (kk & 3) * 2;
+            const uint32_t bo = (kk >> 2) * KC + (kk & 3) * 2;
+            ptx::umma_ss_lohi_if(leader, s_tmem, q_lo + ao,
+                                 k_lo + static_cast<uint32_t>((sk % NST) * C::KV_BYTES >> 4) + bo, HI, C::IDESC_S,
+                                 kk > 0 ? 1u : 0u);
+          }
+          commit(C::B_SFULL + s);
+          commit(C::B_EMPTY + sk % NST);
+          if (sole) commit(C::B_EMPTY + sk % NST);
+          if (j == nj - 1) commit(C::B_QEMPTY + s);
+          // with ranges, the V tile once warp 11 has passed it
+          if (!wait(C::B_FULL + sv % NST, sv / NST) || (a.ranges && !wait(S::B_VOK + sv % NST, sv / NST))) {
+            ok = false;
+            break;
+          }
+          const uint32_t vb = v_lo + static_cast<uint32_t>((sv % NST) * C::KV_BYTES >> 4);
+#pragma unroll
+          for (int q = 0; q < C::NPV; ++q) {
+            if (!wait(C::B_PFULL + s * C::NPV + q, tcnt)) {
+              ok = false;
+              break;
+            }
+            ptx::tc_fence_after();
+#pragma unroll
+            for (int u = 0; u < KPP; ++u) {
+              const int kk = q * KPP + u;
+              ptx::umma_ts_lohi_if(leader, o_tmem, s_tmem + kk * 8, vb + kk * (2048 >> 4), HI, C::IDESC_PV,
+                                   (j > 0 || kk > 0) ? 1u : 0u);
+            }
+          }
+          if (!ok) break;
+          commit(C::B_PVDONE + s);
+          commit(C::B_EMPTY + sv % NST);
+          if (sole) commit(C::B_EMPTY + sv % NST);
+          ++tcnt;
+        }
+        if (!ok) break;
+      }
+      if (!ok) {
+        commit(C::B_DRAIN + s);
+        volatile int dummy = 0;
+        ptx::mbar_wait(bar(C::B_DRAIN + s), 0, &dummy, a.timeout_ns / 4, 0);
+        __syncwarp();
+      }
+    } else {
+      // ============================================================ warp 11: V rows that no row sees
+      // B_VOK counts every use of a stage, K tiles included, so that its
+      // parity is the stage's; its arrival comes before the one on B_EMPTY, so
+      // a use's B_FULL implies that all earlier B_VOK phases are complete.
+      int seq = 0;
+      bool ok = true;
+      for (int np = 0; ok; ++np) {
+        if (!wait(C::B_WFULL + (np & 1), np >> 1)) break;
+        const int w = turn[3 * (np & 1)], j0 = turn[3 * (np & 1) + 1], nj = turn[3 * (np & 1) + 2];
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(bar(C::B_WEMPTY + (np & 1)));
+        if (w >= n_pairs) break;
+        if (!a.ranges) continue;
+        const ScoredPair pr = scored_pair(a, w, nph);
+        int2 rg[8];  // the ranges of my eight rows of the pair
+#pragma unroll
+        for (int u = 0; u < 8; ++u)
+          rg[u] = (u < 4 || pr.has1) ? scored_range(a, pr.q0 * 128 + u * 32 + lane, false) : make_int2(0, 0);
+        for (int j = 0; j < nj; ++j, seq += 2) {
+          const int st_k = seq % NST, st = (seq + 1) % NST;
+          if (!wait(C::B_FULL + st_k, seq / NST)) {
+            ok = false;
+            break;
+          }
+          if (lane == 0) {
+            ptx::mbar_arrive(bar(S::B_VOK + st_k));
+            ptx::mbar_arrive(bar(C::B_EMPTY + st_k));
+          }
+          if (!wait(C::B_FULL + st, (seq + 1) / NST)) {
+            ok = false;
+            break;
+          }
+          const int c0 = (j0 + j) * BK;
+          bool whole = false;
+#pragma unroll
+          for (int u = 0; u < 8; ++u) whole |= rg[u].x <= c0 && rg[u].y >= c0 + BK;
+          if (!__any_sync(0xffffffffu, whole)) {
+            uint32_t seen[4] = {0, 0, 0, 0};  // bit per key of the tile
+#pragma unroll
+            for (int u = 0; u < 8; ++u) {
+#pragma unroll
+              for (int q = 0; q < 4; ++q) {
+                const int f = min(max(rg[u].x - c0 - 32 * q, 0), 32), t = min(max(rg[u].y - c0 - 32 * q, 0), 32);
+                if (f < t) seen[q] |= (0xffffffffu >> (32 - (t - f))) << f;
+              }
+            }
+            bool cleared = false;
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+              const uint32_t all = __reduce_or_sync(0xffffffffu, seen[q]);
+              if (!((all >> lane) & 1u)) {
+                uint8_t* row = smem + C::OFF_RING + st * C::KV_BYTES + (32 * q + lane) * 128;
+#pragma unroll
+                for (int c = 0; c < C::DCH; ++c)
+#pragma unroll
+                  for (int x = 0; x < 8; ++x)
+                    *reinterpret_cast<uint4*>(row + c * C::KV_CHUNK + x * 16) = make_uint4(0, 0, 0, 0);
+                cleared = true;
+              }
+            }
+            if (cleared) asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+          }
+          __syncwarp();
+          if (lane == 0) {
+            ptx::mbar_arrive(bar(S::B_VOK + st));
+            ptx::mbar_arrive(bar(C::B_EMPTY + st));
+          }
+        }
+      }
+    }
+  } else {
+    // ================================================================ softmax
+    setmaxnreg_inc_224();
+    const int slot = warp >> 2;
+    const int wq = warp & 3;
+    const int r = wq * 32 + lane;  // row == TMEM lane
+    const uint32_t lane_base = tmem + (static_cast<uint32_t>(wq * 32) << 16);
+    const uint32_t s_col = slot ? C::TM_S1 : C::TM_S0;
+    const uint32_t o_col = slot ? C::TM_O1 : C::TM_O0;
+    const float ninf = -__int_as_float(0x7f800000);
+    const uint64_t scale2 = ptx::f32x2(a.scale_log2, a.scale_log2);
+    const uint64_t one2 = ptx::f32x2(1.f, 1.f);
+    uint64_t cap[5];
+    if constexpr (CAP) {
+#pragma unroll
+      for (int u = 0; u < 5; ++u) cap[u] = ptx::f32x2(a.cap_c[u], a.cap_c[u]);
+    }
+    int tcount = 0;  // tiles of this slot so far (SFULL / PVDONE phases)
+    bool ok = true;
+    for (int np = 0; ok; ++np) {
+      if (!ptx::mbar_wait_warp(bar(C::B_WFULL + (np & 1)), (np >> 1) & 1, abort_flag, a.timeout_ns, kErrTimeout)) {
+        ok = false;
+        break;
+      }
+      const int w = turn[3 * (np & 1)], j0 = turn[3 * (np & 1) + 1], nj = turn[3 * (np & 1) + 2];
+      __syncwarp();
+      if (lane == 0) ptx::mbar_arrive(bar(C::B_WEMPTY + (np & 1)));
+      if (w >= n_pairs) break;
+      const ScoredPair pr = scored_pair(a, w, nph);
+      const int h = pr.h;
+      const int qi = pr.q0 + slot;
+      if (slot == 1 && !pr.has1) continue;
+      const int grow = qi * 128 + r;
+      const bool row_valid = grow < a.L;
+      uint4* o_dst = reinterpret_cast<uint4*>(a.o + (static_cast<long>(h) * a.L + grow) * D);
+      float* lse_dst = a.lse + static_cast<long>(h) * a.L + grow;
+      // my row's keys, and those that all 32 rows of the warp see
+      const int2 rg = scored_range(a, grow, true);
+      const int all_lo = __reduce_max_sync(0xffffffffu, rg.x), all_hi = __reduce_min_sync(0xffffffffu, rg.y);
+      float slope2 = 0.f;
+      if constexpr (BIAS) slope2 = a.slopes[h] * 1.44269504088896340736f;
+      const int at = a.q_start + grow;
+      float m = ninf;  // running row max, log2 units
+      float l = 0.f;   // running row sum
+      for (int jj = 0; jj < nj; ++jj, ++tcount) {
+        const int c0 = (j0 + jj) * BK;
+        if (!ptx::mbar_wait_warp(bar(C::B_SFULL + slot), tcount & 1, abort_flag, a.timeout_ns, kErrTimeout)) {
+          ok = false;
+          break;
+        }
+        ptx::tc_fence_after();
+        float s[BK];
+        {
+          uint32_t raw[BK / 32][32];
+#pragma unroll
+          for (int c = 0; c < BK / 32; ++c) ptx::tmem_ld32(lane_base + s_col + c * 32, raw[c]);
+          ptx::tmem_wait_ld();
+#pragma unroll
+          for (int c = 0; c < BK / 32; ++c) {
+            ptx::reg_fence32(raw[c]);
+#pragma unroll
+            for (int e = 0; e < 32; ++e) s[c * 32 + e] = __uint_as_float(raw[c][e]);
+          }
+        }
+        const bool masked = c0 < all_lo || c0 + BK > all_hi;  // warp-uniform
+        // `raw_args`: s stays raw and the exp pass applies the scale or the
+        // polynomial; otherwise s is brought to log2 units here
+        bool raw_args = true;
+        float mx;
+        if constexpr (CAP) {
+          const float top = row_max(s), low = row_min(s);
+          const bool wide = __any_sync(0xffffffffu, fmaxf(top, -low) > a.cap_fast);
+          raw_args = !wide && !masked && !BIAS;
+          if (raw_args) {
+            float y0, y1;
+            const uint64_t v = ptx::f32x2(top, top);
+            ptx::f32x2_split(mul_f32x2(v, cap_poly(v, cap)), y0, y1);
+            mx = y0;  // the polynomial rises with s
+          } else if (wide) {
+#pragma unroll
+            for (int c = 0; c < BK; ++c) s[c] = a.cap_log2 * tanh_wide(s[c] * a.cap_in);
+          } else {
+#pragma unroll
+            for (int c = 0; c < BK; c += 2) {
+              const uint64_t v = ptx::f32x2(s[c], s[c + 1]);
+              ptx::f32x2_split(mul_f32x2(v, cap_poly(v, cap)), s[c], s[c + 1]);
+            }
+          }
+        } else if constexpr (BIAS) {
+          raw_args = false;
+#pragma unroll
+          for (int c = 0; c < BK; c += 2)
+            ptx::f32x2_split(mul_f32x2(ptx::f32x2(s[c], s[c + 1]), scale2), s[c], s[c + 1]);
+        }
+        if constexpr (BIAS) {
+          const int at0 = at - lane;  // the warp's first row
+          add_bias(s, slope2, at, c0, c0 + BK - 1 <= at0 ? -1 : (c0 >= at0 + 31 ? 1 : 0));
+        }
+        if (masked) {
+#pragma unroll
+          for (int c = 0; c < BK; ++c)
+            if (c0 + c < rg.x || c0 + c >= rg.y) s[c] = ninf;
+        }
+        if constexpr (CAP) {
+          if (!raw_args) mx = row_max(s);
+        } else {
+          mx = row_max(s);
+          if constexpr (!BIAS) mx *= a.scale_log2;  // scale_log2 > 0
+        }
+        const float m_new = fmaxf(m, mx);
+        if (jj == 0) {
+          m = m_new;
+        } else if (__any_sync(0xffffffffu, m_new > m + 8.0f)) {
+          // O_s holds every earlier tile of this item: rescale my row (a row
+          // that saw nothing yet has zeros)
+          const float alpha = m_new == ninf ? 1.0f : ptx::ex2(m - m_new);
+#pragma unroll
+          for (int c = 0; c < D / 32; ++c) {
+            uint32_t raw[32];
+            ptx::tmem_ld32(lane_base + o_col + c * 32, raw);
+            ptx::tmem_wait_ld();
+            ptx::reg_fence32(raw);
+#pragma unroll
+            for (int e = 0; e < 32; ++e) raw[e] = __float_as_uint(__uint_as_float(raw[e]) * alpha);
+            ptx::tmem_st32(lane_base + o_col + c * 32, raw);
+          }
+          l *= alpha;
+          m = m_new;
+        }
+        const float mu = m == ninf ? 0.f : m;
+        const uint64_t negm2 = ptx::f32x2(-mu, -mu);
+        uint64_t acc0 = ptx::f32x2(0.f, 0.f), acc1 = acc0;
+        constexpr int CPP = BK / 32 / C::NPV;  // 32-column chunks per part of P
+        auto exp_pass = [&](auto capped, uint64_t mul2) {
+#pragma unroll
+          for (int c = 0; c < BK / 32; ++c) {
+            uint32_t pk[16];
+            scored_exp32<decltype(capped)::value>(s + 32 * c, mul2, negm2, cap, pk, acc0, acc1);
+            ptx::tmem_st32_16(lane_base + s_col + c * 16, pk);
+            if ((c + 1) % CPP == 0 && c + 1 < BK / 32) {
+              // this part of P is in TMEM: its PV MMAs may start
+              ptx::tmem_wait_st();
+              ptx::tc_fence_before();
+              __syncwarp();
+              if (lane == 0) ptx::mbar_arrive(bar(C::B_PFULL + slot * C::NPV + c / CPP));
+            }
+          }
+        };
+        if constexpr (CAP) {
+          if (!BIAS && raw_args) exp_pass(std::true_type{}, one2);
+          else exp_pass(std::false_type{}, one2);
+        } else if constexpr (BIAS) {
+          exp_pass(std::false_type{}, one2);
+        } else {
+          exp_pass(std::false_type{}, scale2);
+        }
+        float a0, a1, b0, b1;
+        ptx::f32x2_split(acc0, a0, a1);
+        ptx::f32x2_split(acc1, b0, b1);
+        l += (a0 + b0) + (a1 + b1);
+        ptx::tmem_wait_st();
+        ptx::tc_fence_before();
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(bar(C::B_PFULL + slot * C::NPV + C::NPV - 1));
+      }
+      if (!ok) break;
+      if (nj == 0) {
+        if (row_valid) {
+#pragma unroll
+          for (int c = 0; c < D / 8; ++c) o_dst[c] = make_uint4(0, 0, 0, 0);
+          *lse_dst = ninf;
+        }
+        continue;
+      }
+      // ---- epilogue: every PV of the item is done -> O / l -> bf16 -> global; LSE
+      if (!ptx::mbar_wait_warp(bar(C::B_PVDONE + slot), (tcount - 1) & 1, abort_flag, a.timeout_ns, kErrTimeout)) {
+        ok = false;
+        break;
+      }
+      ptx::tc_fence_after();
+      const bool empty = l == 0.f;  // the row saw nothing
+      const float inv_l = empty ? 0.f : 1.0f / l;
+#pragma unroll
+      for (int c = 0; c < D / 32; ++c) {
+        uint32_t raw[32];
+        ptx::tmem_ld32(lane_base + o_col + c * 32, raw);
+        ptx::tmem_wait_ld();
+        ptx::reg_fence32(raw);
+        uint32_t pk[16];
+#pragma unroll
+        for (int e = 0; e < 16; ++e)
+          pk[e] = empty ? 0u
+                        : ptx::pack_bf16x2(__uint_as_float(raw[2 * e]) * inv_l, __uint_as_float(raw[2 * e + 1]) * inv_l);
+        if (row_valid) {
+#pragma unroll
+          for (int u = 0; u < 4; ++u)
+            o_dst[c * 4 + u] = make_uint4(pk[4 * u], pk[4 * u + 1], pk[4 * u + 2], pk[4 * u + 3]);
+        }
+      }
+      if (row_valid) *lse_dst = empty ? ninf : (m + ptx::lg2(l)) * 0.69314718055994530942f;
+      // the next item's first PV overwrites O_s only after this warp's next
+      // PFULL arrival, which follows the loads above (tcgen05.wait::ld)
+    }
+  }
+
+  ptx::tc_fence_before();
+  __syncthreads();
+  if (warp == 9) {
+    ptx::tc_fence_after();
+    ptx::tmem_dealloc(tmem, C::TM_ALLOC);
+  }
+}
+
+}  // namespace sparsed

@@ -37,6 +37,78 @@ int check_mod(float scale, float softcap, const float* slopes) {
   return SPARSED_OK;
 }
 
+// [H, L, d] bf16 with strides (in elements) as a 3-D tensor map, boxes of 64
+// columns x rows.
+int make_map_strided(CUtensorMap* m, const void* ptr, int H, int L, int d, size_t stride_h, size_t stride_l,
+                     int box_rows) {
+  cuuint64_t dims[3] = {static_cast<cuuint64_t>(d), static_cast<cuuint64_t>(L), static_cast<cuuint64_t>(H)};
+  // the stride of a dimension of one says nothing
+  cuuint64_t strides[2] = {static_cast<cuuint64_t>(L > 1 ? stride_l : d) * 2,
+                           static_cast<cuuint64_t>(H > 1 ? stride_h : d) * 2};
+  cuuint32_t box[3] = {64, static_cast<cuuint32_t>(box_rows), 1};
+  cuuint32_t es[3] = {1, 1, 1};
+  CUresult r = g_encode(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(ptr), dims, strides, box, es,
+                        CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                        CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS) return fail_cuda(cudaErrorInvalidValue);
+  return SPARSED_OK;
+}
+
+// A strided [H, L, d] operand that a tensor map can describe: strides of 16
+// bytes' multiples, not 0 (a broadcast head is fewer kv heads instead).
+int check_map_strides(int H, int L, size_t stride_h, size_t stride_l) {
+  if (((stride_h | stride_l) & 7u) != 0) return SPARSED_ERR_INVALID_ARG;
+  if ((H > 1 && stride_h == 0) || (L > 1 && stride_l == 0)) return SPARSED_ERR_INVALID_ARG;
+  if (stride_h >= (1ull << 38) || stride_l >= (1ull << 38)) return SPARSED_ERR_UNSUPPORTED;
+  return SPARSED_OK;
+}
+
+struct ScoredMaps {
+  CUtensorMap q, k, v;
+};
+
+template <int D, bool CAP, bool BIAS>
+int launch_scored_t(const ScoredMaps& t, const ScoredArgs& a, int grid, cudaStream_t st) {
+  using C = AttnCfg<D, 128>;
+  auto kern = scored_attn_kernel<D, CAP, BIAS>;
+  // the register split must be funded by the launch (as launch_attn_t)
+  static int regs = -1;
+  if (regs < 0) {
+    cudaFuncAttributes fa;
+    SP_CUDA(cudaFuncGetAttributes(&fa, kern));
+    regs = fa.numRegs;
+  }
+  if (regs * C::THREADS < C::REGS_SOFTMAX * 256 + C::REGS_OTHER * (C::THREADS - 256)) return SPARSED_ERR_UNSUPPORTED;
+  SP_CUDA(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, ScoredCfg<D>::SMEM_BYTES));
+  kern<<<grid, C::THREADS, ScoredCfg<D>::SMEM_BYTES, st>>>(t.q, t.k, t.v, a);
+  SP_CUDA(cudaGetLastError());
+  return SPARSED_OK;
+}
+
+template <int D>
+int launch_scored(const ScoredMaps& t, const ScoredArgs& a, bool cap, int grid, cudaStream_t st) {
+  if (cap) return a.slopes ? launch_scored_t<D, true, true>(t, a, grid, st) : launch_scored_t<D, true, false>(t, a, grid, st);
+  return a.slopes ? launch_scored_t<D, false, true>(t, a, grid, st) : launch_scored_t<D, false, false>(t, a, grid, st);
+}
+
+// Capped scores in log2 units: y = s * P(s^2) while |s| * scale / cap <= 0.6,
+// with tanh(u) = u * (c0 + c1 u^2 + ... + c4 u^8) to 2e-8 there (minimax fit).
+void cap_coefficients(float scale, float softcap, float (&c)[5], float* fast, float* in, float* cap_log2) {
+  constexpr double kC[5] = {0.9999996274072432, -0.3333120858238067, 0.13299210120915597, -0.051696738736441226,
+                            0.014976954257328949};
+  const double u = static_cast<double>(scale) / softcap, cl = softcap * 1.4426950408889634;
+  double f = cl * u;
+  bool finite = true;
+  for (int i = 0; i < 5; ++i, f *= u * u) {
+    c[i] = static_cast<float>(kC[i] * f);
+    finite = finite && std::isfinite(c[i]);
+  }
+  *in = static_cast<float>(u);
+  *cap_log2 = static_cast<float>(cl);
+  // above this the wide form; everywhere if the polynomial does not fit fp32
+  *fast = !finite ? -1.f : (u > 0 && 0.6 / u < 1e18 ? static_cast<float>(0.6 / u) : 1e18f);
+}
+
 }  // namespace
 
 extern "C" {
@@ -225,44 +297,57 @@ int sparsed_scored_attn(const uint16_t* Q, size_t q_stride_h, size_t q_stride_l,
   if (d != 64 && d != 128) return SPARSED_ERR_UNSUPPORTED;
   if (Hq == 0 || Lq == 0) return SPARSED_OK;
   if (Hkv == 0 || Hq % Hkv != 0) return SPARSED_ERR_INVALID_ARG;
-  if (Hq > 65535 || Lq > (1 << 30) || Lk > (1 << 30) || q_start > (1 << 30) || q_start < -(1 << 30))
+  if (Hq > 65535 || Lq > (1 << 29) || Lk > (1 << 29) || q_start > (1 << 29) || q_start < -(1 << 29))
     return SPARSED_ERR_UNSUPPORTED;
   if (!Q || !O || !LSE || (Lk > 0 && (!K || !V))) return SPARSED_ERR_INVALID_ARG;
   if (!aligned16(Q) || !aligned16(K) || !aligned16(V) || !aligned16(O) || !aligned4(LSE) ||
       (reinterpret_cast<uintptr_t>(ranges) & 7u))
     return SPARSED_ERR_INVALID_ARG;
-  if (((q_stride_h | q_stride_l | k_stride_h | k_stride_l | v_stride_h | v_stride_l) & 7u) != 0)
-    return SPARSED_ERR_INVALID_ARG;
+  SP_TRY(check_map_strides(Hq, Lq, q_stride_h, q_stride_l));
+  SP_TRY(check_map_strides(Hkv, Lk, k_stride_h, k_stride_l));
+  SP_TRY(check_map_strides(Hkv, Lk, v_stride_h, v_stride_l));
   size_t need = 0;
   SP_TRY(sparsed_scored_attn_workspace_bytes(Hq, Lq, &need));
   if (!workspace || workspace_bytes < need || (reinterpret_cast<uintptr_t>(workspace) & 255u)) return SPARSED_ERR_WORKSPACE;
   SP_TRY(require_sm100());
-  RowsArgs a = {};
-  a.q = Q;
-  a.qs_h = q_stride_h;
-  a.qs_b = q_stride_l;
-  a.k = K;
-  a.v = V;
-  a.ks_h = k_stride_h;
-  a.ks_l = k_stride_l;
-  a.vs_h = v_stride_h;
-  a.vs_l = v_stride_l;
-  a.N = 1;
-  a.Hq = Hq;
-  a.Hkv = Hkv;
-  a.B = Lq;
+  SP_TRY(get_encoder());
+  ScoredMaps t;
+  SP_TRY(make_map_strided(&t.q, Q, Hq, Lq, d, q_stride_h, q_stride_l, 128));
+  if (Lk > 0) {
+    SP_TRY(make_map_strided(&t.k, K, Hkv, Lk, d, k_stride_h, k_stride_l, 128));
+    SP_TRY(make_map_strided(&t.v, V, Hkv, Lk, d, v_stride_h, v_stride_l, 128));
+  } else {
+    t.k = t.v = t.q;  // no key, no tile is read
+  }
+  int sms = 0;
+  SP_TRY(sm_count(&sms));
+  ScoredArgs a = {};
+  a.H = Hq;
+  a.group = Hq / Hkv;
+  a.L = Lq;
   a.Lk = Lk;
-  a.q_start0 = q_start;
-  a.ranges = ranges;
-  a.mod = ScoreMod{scale, softcap, slopes};
-  a.o = O;
+  a.nqb = static_cast<int>(cdiv(Lq, 128));
+  // tiles in pairs share K/V tiles; single ones while each can have its own SM
+  a.qpp = static_cast<long>(Hq) * a.nqb <= sms ? 1 : 2;
+  const long turns = static_cast<long>(Hq) * cdiv(a.nqb, a.qpp);
+  if (turns >= (1l << 31) - sms) return SPARSED_ERR_UNSUPPORTED;
+  a.scale_log2 = scale * 1.44269504088896340736f;
+  if (a.scale_log2 < 1.17549435e-38f) a.scale_log2 = 1.17549435e-38f;  // 0 would turn a masked -inf into NaN
+  a.slopes = slopes;
+  a.q_start = q_start;
+  a.ranges = reinterpret_cast<const int2*>(ranges);
+  if (softcap > 0.f) cap_coefficients(scale, softcap, a.cap_c, &a.cap_fast, &a.cap_in, &a.cap_log2);
   a.lse = LSE;
-  const dim3 grid(Lq, Hq, 1);
+  a.o = O;
+  a.timeout_ns = kWaitTimeoutNs;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  if (d == 64) score_rows_kernel<64><<<grid, 128, 0, st>>>(a);
-  else score_rows_kernel<128><<<grid, 128, 0, st>>>(a);
-  SP_CUDA(cudaGetLastError());
-  return SPARSED_OK;
+  // more turns than CTAs: later ones are claimed from a counter
+  if (turns > sms) {
+    a.sched = static_cast<int*>(workspace);
+    SP_CUDA(cudaMemsetAsync(a.sched, 0, sizeof(int), st));
+  }
+  const int grid = static_cast<int>(turns < sms ? turns : sms);
+  return d == 64 ? launch_scored<64>(t, a, softcap > 0.f, grid, st) : launch_scored<128>(t, a, softcap > 0.f, grid, st);
 }
 
 }  // extern "C"

@@ -23,6 +23,7 @@
 #include "rope_kernels.cuh"
 #include "cache_kernels.cuh"
 #include "score_rows_kernel.cuh"
+#include "scored_kernel.cuh"
 
 using namespace sparsed;
 
