@@ -13,8 +13,8 @@ INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libsparsed.so")
 SOURCES = ["sparsed_api.cu"]
 DEPS = ["sparsed_api.cu", "attn_kernel.cuh", "attn_list_kernel.cuh", "select_kernels.cuh", "column_kernels.cuh", "losa_kernels.cuh",
-        "ptx_sm100.cuh", "rope_kernels.cuh", "cache_kernels.cuh", "score_rows_kernel.cuh",
-        "scored_kernel.cuh", "serve_api.cuh"]
+        "ptx_sm100.cuh", "rope_kernels.cuh", "cache_kernels.cuh", "scored_kernel.cuh",
+        "cache_attn_kernel.cuh", "serve_api.cuh"]
 
 
 def nvcc_path() -> str:

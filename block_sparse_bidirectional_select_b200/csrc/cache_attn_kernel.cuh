@@ -1,0 +1,847 @@
+// Attention over the 8-bit cache for sm_100a: the query tokens of each sequence
+// (one token, or a block being denoised) against all its cached keys.
+//
+//   x = scale * <q, k>, k = e4m3 * 2^ek;  capped, biased as scored_attn
+//   O = sum softmax(x)_c v_c,  v = e4m3 * 2^ev
+//
+// Rows. A kv head's query rows (its query heads times B tokens) are cut into
+// row tiles of up to 128; an item is one row tile of one kv head of one
+// sequence. Its keys are walked in tiles of 128 (two scale blocks).
+//
+// Work split. All key tiles of all items, in order, are dealt out as one run
+// of equal length per CTA, whatever the sequences' lengths, so every SM reads
+// the same number of bytes. A CTA's run crosses item boundaries; an item cut by
+// a run's end leaves partial results (O normalised, log2 of the sum) that
+// cache_merge_kernel joins in the order of the runs: no atomics, the same bits
+// every time.
+//
+// Exact operands. e4m3 has 4 significant bits and bf16 has 8, so a bf16 query
+// is the sum of two e4m3 numbers: hi = e4m3(q 2^-e), lo = e4m3(q 2^-e - hi),
+// with 2^e the row's own scale. lo is exact while the element is at least 2^-2
+// of the row's scaled range (224..448 at its top); below, it is off by
+// 2^-10, 2^-17.8 of the row's largest element. S = hi K^T + lo K^T runs on the
+// fp8 tensor path straight from the cached bytes, at the cost of one bf16
+// product. For P V that trick would lose the tail of a peaked row (a weight
+// below 2^-10 of the largest has no bits left in e4m3), so V is widened to
+// f16, exactly, and P is f16 with its top at 2^7 .. 2^15 (error 2^-11, or
+// 2^-32 of the largest weight). Each V block is brought to the largest scale of
+// the run's part of the item (a power of two: exact, or below 2^-24 of that
+// scale), so O accumulates in one unit.
+//
+// Warp roles (512 threads):
+//   warps 0-7   softmax: warp w covers rows 32*(w%4) + 16*(w/4) + 0..15, thread t
+//               row t%16 and key half t/16 (one scale block) of every tile; they
+//               also bring each item's Q into TMEM as hi and lo
+//   warp 8      TMA producer: K and V tiles
+//   warp 9      TMEM owner; issues S
+//   warp 10     issues O += P V
+//   warp 11     idle
+//   warps 12-15 widen V tiles (e4m3 -> f16, rows past the length cleared)
+// TMEM: [S0 | S1 | O | Q0 | Q1], P over the first half of its S.
+// Barriers and orders otherwise as attn_list_kernel. Every wait is bounded.
+#pragma once
+
+#include "cache_kernels.cuh"
+#include "scored_kernel.cuh"
+
+namespace sparsed {
+
+constexpr int kCacheTile = 128;
+constexpr int kCacheMaxCtas = 160;
+constexpr float kPShift = 7.0f;  // P's top is 2^7 when its row maximum is fresh
+
+struct CacheArgs {
+  const uint16_t* q;
+  size_t qs_n, qs_h, qs_b;
+  const float *k_scale, *v_scale;  // [N, Hkv, C/64]
+  const int32_t* lengths;
+  const int32_t* q_start;          // or null
+  int N, Hkv, group, B, C;
+  int R, RT;                       // rows of a kv head, row tiles
+  int part_rows;                   // rows of a partial result's slot
+  float scale_log2;                // above 0
+  const float* slopes;             // or null
+  float cap_c[5];                  // as ScoredArgs
+  float cap_fast, cap_in, cap_log2;
+  int capped;
+  uint16_t* o;                     // [N, Hkv * group, B, D]
+  float* lse;
+  float* o_part;                   // [2 * CTAs][part_rows][D]
+  float* l_part;                   // [2 * CTAs][part_rows], log2 units
+  uint64_t timeout_ns;
+};
+
+template <int D>
+struct CacheCfg {
+  static constexpr int BK = kCacheTile;
+  static constexpr int HALF = 64;
+  static constexpr int T8 = BK * D;           // bytes of an e4m3 tile
+  static constexpr int T16 = 2 * T8;
+  static constexpr int KS = D == 128 ? 5 : 8;
+  static constexpr int VS = KS;
+  static constexpr int OFF_K = 0;
+  static constexpr int OFF_V = OFF_K + KS * T8;
+  static constexpr int OFF_W = OFF_V + VS * T8;  // widened V, 2 buffers
+  static constexpr int OFF_BAR = OFF_W + 2 * T16;
+  static constexpr int B_KFULL = 0;
+  static constexpr int B_KEMPTY = B_KFULL + KS;
+  static constexpr int B_VFULL = B_KEMPTY + KS;
+  static constexpr int B_VEMPTY = B_VFULL + VS;  // 4 converter-warp arrivals
+  static constexpr int B_WFULL = B_VEMPTY + VS;  // [2] 4 converter-warp arrivals
+  static constexpr int B_SFULL = B_WFULL + 2;    // [2]
+  static constexpr int B_PFULL = B_SFULL + 2;    // [2] 8 softmax-warp arrivals
+  static constexpr int B_PVDONE = B_PFULL + 2;   // [2] also frees the widened V
+  static constexpr int B_DRAIN = B_PVDONE + 2;   // [2]
+  static constexpr int B_QTFULL = B_DRAIN + 2;   // [2] 8 softmax-warp arrivals
+  static constexpr int B_QTEMPTY = B_QTFULL + 2; // [2]
+  static constexpr int NUM_BARS = B_QTEMPTY + 2;
+  static constexpr int OFF_MISC = OFF_BAR + NUM_BARS * 8;  // tmem slot, abort flag, run
+  static constexpr int SMEM_BYTES = OFF_MISC + 48 + 1024;
+  static constexpr int TM_S0 = 0;
+  static constexpr int TM_S1 = BK;
+  static constexpr int TM_O = 2 * BK;
+  static constexpr int TM_Q0 = 2 * BK + D;  // hi: D/4 columns of four e4m3, lo: D/4
+  static constexpr int TM_Q1 = TM_Q0 + D / 2;
+  static constexpr int TM_ALLOC = 512;
+  // f32 accumulators; e4m3 x e4m3 (kind::f8f6f4) and f16 x f16 (kind::f16) are both format 0
+  static constexpr uint32_t idesc(int N, int b_mn) {
+    return (1u << 4) | (static_cast<uint32_t>(b_mn) << 16) | (static_cast<uint32_t>(N >> 3) << 17) | (8u << 24);
+  }
+  static constexpr uint32_t IDESC_S = idesc(BK, 0);
+  static constexpr uint32_t IDESC_PV = idesc(D, 1);
+  // K rows of D bytes: one swizzle span of 128 or 64 bytes, 8 rows a group
+  static constexpr uint32_t HI_K = ((8u * D) >> 4) | (1u << 14) | ((D == 128 ? 2u : 4u) << 29);
+  static constexpr int THREADS = 512;
+  static constexpr int REGS_SOFTMAX = 184, REGS_CONTROL = 56, REGS_WIDEN = 88;
+  static_assert(TM_Q1 + D / 2 <= 512, "TMEM budget");
+  static_assert(SMEM_BYTES <= 232448, "shared memory budget");
+};
+
+namespace ptx {
+__device__ __forceinline__ void umma_ts_f8_if(uint32_t leader, uint32_t d_tmem, uint32_t a_tmem, uint32_t b_lo,
+                                              uint32_t hi, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t.reg .b64 db;\n\t"
+      "setp.ne.b32 p, %5, 0;\n\t"
+      "setp.ne.b32 q, %6, 0;\n\t"
+      "mov.b64 db, {%2, %3};\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], [%1], db, %4, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_tmem), "r"(b_lo), "r"(hi), "r"(idesc), "r"(accumulate), "r"(leader)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st32_8(uint32_t taddr, const uint32_t (&r)[8]) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr), "r"(r[0]),
+               "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+               : "memory");
+}
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+__device__ __forceinline__ void setmaxnreg_inc_184() { asm volatile("setmaxnreg.inc.sync.aligned.u32 184;" ::: "memory"); }
+__device__ __forceinline__ void setmaxnreg_dec_88() { asm volatile("setmaxnreg.dec.sync.aligned.u32 88;" ::: "memory"); }
+}  // namespace ptx
+
+__device__ __forceinline__ int cache_len(const CacheArgs& a, int n) { return min(max(a.lengths[n], 0), a.C); }
+__device__ __forceinline__ int cache_tiles(int len) { return (len + kCacheTile - 1) / kCacheTile; }
+
+// Total key tiles of the call, and those before sequence n_stop (one warp).
+__device__ __forceinline__ long cache_total(const CacheArgs& a, int lane, int n_stop, long* before) {
+  long t = 0, b = 0;
+  for (int n = lane; n < a.N; n += 32) {
+    const long x = static_cast<long>(cache_tiles(cache_len(a, n))) * a.Hkv * a.RT;
+    t += x;
+    if (n < n_stop) b += x;
+  }
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) {
+    t += __shfl_xor_sync(0xffffffffu, t, off);
+    b += __shfl_xor_sync(0xffffffffu, b, off);
+  }
+  if (before) *before = b;
+  return t;
+}
+
+// First tile of run c of G runs over T tiles.
+__device__ __forceinline__ long run_begin(long T, int c, int G) {
+  const long q = T / G, r = T - q * G;
+  return q * c + (r * c) / G;
+}
+
+// A run's parts: the tiles of one item that lie in it.
+struct CachePart {
+  int n, hk, rt;   // item
+  int len;         // the sequence's length
+  int nt;          // the item's tiles
+  int t0, cnt;     // this part's tiles
+};
+struct CacheRun {
+  int n, len, nt;
+  long off, left;
+  __device__ __forceinline__ void load(const CacheArgs& a) {
+    len = cache_len(a, n);
+    nt = cache_tiles(len);
+  }
+  __device__ __forceinline__ bool next(const CacheArgs& a, CachePart* p) {
+    if (left <= 0) return false;
+    while (off >= static_cast<long>(nt) * a.Hkv * a.RT) {
+      off = 0;
+      ++n;
+      if (n >= a.N) return false;
+      load(a);
+    }
+    const int item = static_cast<int>(off / nt);
+    p->n = n;
+    p->hk = item / a.RT;
+    p->rt = item - p->hk * a.RT;
+    p->len = len;
+    p->nt = nt;
+    p->t0 = static_cast<int>(off - static_cast<long>(item) * nt);
+    p->cnt = static_cast<int>(min(static_cast<long>(nt - p->t0), left));
+    off += p->cnt;
+    left -= p->cnt;
+    return true;
+  }
+};
+
+// The largest exponent among the part's V scales (one warp).
+__device__ __forceinline__ int part_vref(const CacheArgs& a, const CachePart& p, int lane) {
+  const float* vs = a.v_scale + (static_cast<long>(p.n) * a.Hkv + p.hk) * (a.C / kCacheBlock);
+  const int b0 = 2 * p.t0, b1 = min(2 * (p.t0 + p.cnt), (p.len + kCacheBlock - 1) / kCacheBlock);
+  int e = kCacheEMin;
+  for (int b = b0 + lane; b < b1; b += 32) e = max(e, scale_exponent(vs[b]));
+  return __reduce_max_sync(0xffffffffu, e);
+}
+
+template <int D, bool MOD>
+__global__ void __launch_bounds__(512, 1)
+    cache_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
+                      const __grid_constant__ CacheArgs a) {
+  using C = CacheCfg<D>;
+  constexpr int HALF = C::HALF;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                             ~static_cast<uintptr_t>(1023));
+  const uint32_t sb = ptx::smem_u32(smem);
+  const int warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::OFF_MISC);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::OFF_MISC + 4);
+  volatile long* run_s = reinterpret_cast<volatile long*>(smem + C::OFF_MISC + 8);  // sequence, tile in it, tiles
+  auto bar = [&](int idx) -> uint32_t { return sb + C::OFF_BAR + 8 * idx; };
+
+  // ---- setup
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < C::KS; ++s) {
+      ptx::mbar_init(bar(C::B_KFULL + s), 1);
+      ptx::mbar_init(bar(C::B_KEMPTY + s), 1);
+      ptx::mbar_init(bar(C::B_VFULL + s), 1);
+      ptx::mbar_init(bar(C::B_VEMPTY + s), 4);
+    }
+    for (int b = 0; b < 2; ++b) {
+      ptx::mbar_init(bar(C::B_WFULL + b), 4);
+      ptx::mbar_init(bar(C::B_SFULL + b), 1);
+      ptx::mbar_init(bar(C::B_PFULL + b), 8);
+      ptx::mbar_init(bar(C::B_PVDONE + b), 1);
+      ptx::mbar_init(bar(C::B_DRAIN + b), 1);
+      ptx::mbar_init(bar(C::B_QTFULL + b), 8);
+      ptx::mbar_init(bar(C::B_QTEMPTY + b), 1);
+    }
+    *abort_flag = 0;
+    ptx::fence_mbar_init();
+  }
+  if (warp == 9) {
+    ptx::tmem_alloc(ptx::smem_u32(tmem_slot), C::TM_ALLOC);
+    ptx::tmem_relinquish();
+  }
+  if (warp == 12) {
+    // my run: its first tile's sequence, and the tile within the sequence
+    const long T = cache_total(a, lane, 0, nullptr);
+    const long begin = run_begin(T, blockIdx.x, gridDim.x), end = run_begin(T, blockIdx.x + 1, gridDim.x);
+    long base = 0;
+    int n0 = a.N;
+    for (int nb = 0; nb < a.N && begin < end; nb += 32) {
+      const int n = nb + lane;
+      const long x = n < a.N ? static_cast<long>(cache_tiles(cache_len(a, n))) * a.Hkv * a.RT : 0;
+      long inc = x;
+#pragma unroll
+      for (int off = 1; off < 32; off <<= 1) {
+        const long y = __shfl_up_sync(0xffffffffu, inc, off);
+        if (lane >= off) inc += y;
+      }
+      const uint32_t hit = __ballot_sync(0xffffffffu, base + inc > begin);
+      if (hit) {
+        const int src = __ffs(hit) - 1;
+        n0 = nb + src;
+        base += __shfl_sync(0xffffffffu, inc - x, src);
+        break;
+      }
+      base += __shfl_sync(0xffffffffu, inc, 31);
+    }
+    if (lane == 0) {
+      run_s[0] = n0 < a.N ? n0 : 0;
+      run_s[1] = begin - base;
+      run_s[2] = n0 < a.N ? end - begin : 0;
+    }
+  }
+  ptx::tc_fence_before();
+  __syncthreads();
+  ptx::tc_fence_after();
+  ptx::grid_dep_launch();
+  const uint32_t tmem = *tmem_slot;
+  CacheRun run;
+  run.n = static_cast<int>(run_s[0]);
+  run.off = run_s[1];
+  run.left = run_s[2];
+  if (run.left > 0) run.load(a);
+  CachePart part;
+
+  if (warp >= 12) {
+    // ================================================================ widen V
+    ptx::setmaxnreg_dec_88();
+    const int tid = threadIdx.x - 384;
+    constexpr int TPR = D / 16;            // threads of a row, 16 values each
+    constexpr int ROWS = 128 / TPR;        // rows of a pass
+    constexpr int NP = C::BK / ROWS;
+    const int j = tid % TPR, row0 = tid / TPR;
+    const int chunk = j >> 2;
+    // the two 16-byte units of a thread; odd chunks write the second first, so
+    // that eight threads of a row cover all banks
+    const int ua = 2 * (j & 3) + (chunk & 1), ub = ua ^ 1;
+    int g = 0;
+    bool ok = true;
+    while (ok && run.next(a, &part)) {
+      const int vref = part_vref(a, part, lane);
+      const float* vs = a.v_scale + (static_cast<long>(part.n) * a.Hkv + part.hk) * (a.C / kCacheBlock);
+      for (int t = part.t0; t < part.t0 + part.cnt; ++t, ++g) {
+        const int st = g % C::VS, b = g & 1;
+        const int valid = part.len - t * C::BK;
+        // 2^(ev - vref) of both scale blocks as f16 pairs
+        uint32_t mul[2];
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          const int dlt = (x * kCacheBlock < valid ? scale_exponent(vs[2 * t + x]) : kCacheEMin) - vref;
+          const uint32_t hbits = dlt >= -14 ? static_cast<uint32_t>(dlt + 15) << 10
+                                            : (dlt >= -24 ? 1u << (dlt + 24) : 0u);
+          mul[x] = hbits | (hbits << 16);
+        }
+        if (!ptx::mbar_wait_warp(bar(C::B_VFULL + st), (g / C::VS) & 1, abort_flag, a.timeout_ns, kErrTimeout) ||
+            (g >= 2 &&
+             !ptx::mbar_wait_warp(bar(C::B_PVDONE + b), ((g - 2) >> 1) & 1, abort_flag, a.timeout_ns, kErrTimeout))) {
+          ok = false;
+          break;
+        }
+        const uint8_t* src = smem + C::OFF_V + st * C::T8 + j * 16;
+        uint8_t* dst = smem + C::OFF_W + b * C::T16 + chunk * (C::BK * 128);
+        uint4 x[NP];
+#pragma unroll
+        for (int p = 0; p < NP; ++p) x[p] = *reinterpret_cast<const uint4*>(src + (row0 + p * ROWS) * D);
+#pragma unroll
+        for (int p = 0; p < NP; ++p) {
+          const int row = row0 + p * ROWS;
+          const uint32_t w[4] = {x[p].x, x[p].y, x[p].z, x[p].w};
+          const uint32_t m2 = mul[p >= NP / 2 ? 1 : 0];
+          uint32_t h[8];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            asm("{\n\t.reg .b16 l, u;\n\tmov.b32 {l, u}, %2;\n\t"
+                "cvt.rn.f16x2.e4m3x2 %0, l;\n\tcvt.rn.f16x2.e4m3x2 %1, u;\n\t}"
+                : "=r"(h[2 * e]), "=r"(h[2 * e + 1])
+                : "r"(w[e]));
+            asm("mul.rn.f16x2 %0, %0, %1;" : "+r"(h[2 * e]) : "r"(m2));
+            asm("mul.rn.f16x2 %0, %0, %1;" : "+r"(h[2 * e + 1]) : "r"(m2));
+          }
+          if (row >= valid) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) h[e] = 0u;
+          }
+          const bool sw = (chunk & 1) != 0;
+          uint8_t* rp = dst + row * 128;
+          *reinterpret_cast<uint4*>(rp + ((ua ^ (row & 7)) << 4)) =
+              make_uint4(sw ? h[4] : h[0], sw ? h[5] : h[1], sw ? h[6] : h[2], sw ? h[7] : h[3]);
+          *reinterpret_cast<uint4*>(rp + ((ub ^ (row & 7)) << 4)) =
+              make_uint4(sw ? h[0] : h[4], sw ? h[1] : h[5], sw ? h[2] : h[6], sw ? h[3] : h[7]);
+        }
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        __syncwarp();
+        if (lane == 0) {
+          ptx::mbar_arrive(bar(C::B_WFULL + b));
+          ptx::mbar_arrive(bar(C::B_VEMPTY + st));
+        }
+      }
+    }
+  } else if (warp >= 8) {
+    setmaxnreg_dec_56();
+    const uint32_t leader = ptx::elect_one();
+    auto wait = [&](int idx, int parity) -> bool {
+      return ptx::mbar_wait_warp(bar(idx), parity & 1, abort_flag, a.timeout_ns, kErrTimeout);
+    };
+    if (warp == 8) {
+      // ============================================================ producer
+      if (leader) {
+        ptx::tma_prefetch_desc(&tm_k);
+        ptx::tma_prefetch_desc(&tm_v);
+      }
+      int g = 0, issued_k = 0, issued_v = 0;
+      bool ok = true;
+      while (ok && run.next(a, &part)) {
+        const int z = part.n * a.Hkv + part.hk;
+        for (int t = part.t0; t < part.t0 + part.cnt; ++t, ++g) {
+          const int st = g % C::KS;
+          if (g >= C::KS && !wait(C::B_KEMPTY + st, g / C::KS - 1)) {
+            ok = false;
+            break;
+          }
+          ptx::mbar_arrive_expect_tx_if(leader, bar(C::B_KFULL + st), C::T8);
+          ptx::tma_load_3d_if(leader, sb + C::OFF_K + st * C::T8, &tm_k, bar(C::B_KFULL + st), 0, t * C::BK, z);
+          issued_k = g + 1;
+          if (g >= C::VS && !wait(C::B_VEMPTY + st, g / C::VS - 1)) {
+            ok = false;
+            break;
+          }
+          ptx::mbar_arrive_expect_tx_if(leader, bar(C::B_VFULL + st), C::T8);
+          ptx::tma_load_3d_if(leader, sb + C::OFF_V + st * C::T8, &tm_v, bar(C::B_VFULL + st), 0, t * C::BK, z);
+          issued_v = g + 1;
+        }
+      }
+      if (!ok) {
+        // let the copies in flight land before the CTA's shared memory goes away
+        const uint64_t short_ns = a.timeout_ns / 4;
+        volatile int dummy = 0;
+        for (int u = (issued_k > C::KS ? issued_k - C::KS : 0); u < issued_k; ++u)
+          ptx::mbar_wait(bar(C::B_KFULL + u % C::KS), (u / C::KS) & 1, &dummy, short_ns, 0);
+        for (int u = (issued_v > C::VS ? issued_v - C::VS : 0); u < issued_v; ++u)
+          ptx::mbar_wait(bar(C::B_VFULL + u % C::VS), (u / C::VS) & 1, &dummy, short_ns, 0);
+        __syncwarp();
+      }
+    } else if (warp == 9) {
+      // ============================================================ S issuer
+      const uint32_t klo = ptx::sdesc_sw128_lo(sb + C::OFF_K, 16);
+      int g = 0, iq = 0;
+      bool ok = true;
+      while (ok && run.next(a, &part)) {
+        const int qc = iq & 1;
+        if (!wait(C::B_QTFULL + qc, iq >> 1)) {
+          ok = false;
+          break;
+        }
+        const uint32_t q_tmem = tmem + (qc ? C::TM_Q1 : C::TM_Q0);
+        for (int t = 0; t < part.cnt; ++t, ++g) {
+          const int b = g & 1, st = g % C::KS;
+          if (!wait(C::B_KFULL + st, g / C::KS) || (g >= 2 && !wait(C::B_PVDONE + b, (g - 2) >> 1))) {
+            ok = false;
+            break;
+          }
+          ptx::tc_fence_after();
+          const uint32_t b0 = klo + static_cast<uint32_t>(st * C::T8 >> 4);
+          const uint32_t s_tmem = tmem + (b ? C::TM_S1 : C::TM_S0);
+#pragma unroll
+          for (int part2 = 0; part2 < 2; ++part2)
+#pragma unroll
+            for (int kk = 0; kk < D / 32; ++kk)
+              ptx::umma_ts_f8_if(leader, s_tmem, q_tmem + part2 * (D / 4) + kk * 8, b0 + kk * 2, C::HI_K, C::IDESC_S,
+                                 (part2 > 0 || kk > 0) ? 1u : 0u);
+          ptx::umma_commit_if(leader, bar(C::B_SFULL + b));
+          ptx::umma_commit_if(leader, bar(C::B_KEMPTY + st));
+        }
+        if (!ok) break;
+        ptx::umma_commit_if(leader, bar(C::B_QTEMPTY + qc));
+        ++iq;
+      }
+      if (!ok) {
+        ptx::umma_commit_if(leader, bar(C::B_DRAIN));
+        volatile int dummy = 0;
+        ptx::mbar_wait(bar(C::B_DRAIN), 0, &dummy, a.timeout_ns / 4, 0);
+        __syncwarp();
+      }
+    } else if (warp == 10) {
+      // ============================================================ PV issuer
+      constexpr uint32_t HI = ptx::sdesc_sw128_hi(1024);
+      const uint32_t vlo = ptx::sdesc_sw128_lo(sb + C::OFF_W, C::BK * 128);
+      int g = 0;
+      bool ok = true;
+      while (ok && run.next(a, &part)) {
+        for (int t = 0; t < part.cnt; ++t, ++g) {
+          const int b = g & 1;
+          if (!wait(C::B_WFULL + b, g >> 1) || !wait(C::B_PFULL + b, g >> 1)) {
+            ok = false;
+            break;
+          }
+          ptx::tc_fence_after();
+          const uint32_t b0 = vlo + static_cast<uint32_t>(b * C::T16 >> 4);
+          const uint32_t p_tmem = tmem + (b ? C::TM_S1 : C::TM_S0);
+#pragma unroll
+          for (int kk = 0; kk < C::BK / 16; ++kk)
+            ptx::umma_ts_lohi_if(leader, tmem + C::TM_O, p_tmem + kk * 8, b0 + kk * (2048 >> 4), HI, C::IDESC_PV,
+                                 (t > 0 || kk > 0) ? 1u : 0u);
+          ptx::umma_commit_if(leader, bar(C::B_PVDONE + b));
+        }
+      }
+      if (!ok) {
+        ptx::umma_commit_if(leader, bar(C::B_DRAIN + 1));
+        volatile int dummy = 0;
+        ptx::mbar_wait(bar(C::B_DRAIN + 1), 0, &dummy, a.timeout_ns / 4, 0);
+        __syncwarp();
+      }
+    }
+  } else {
+    // ================================================================ softmax
+    ptx::setmaxnreg_inc_184();
+    const int half = lane >> 4;
+    const int quad = warp & 3, hw = warp >> 2;
+    const int r = quad * 32 + hw * 16 + (lane & 15);  // row == TMEM lane
+    const uint32_t lane_base = tmem + (static_cast<uint32_t>(quad * 32 + hw * 16) << 16);
+    const float ninf = -__int_as_float(0x7f800000);
+    uint64_t cap[5];
+    if constexpr (MOD) {
+#pragma unroll
+      for (int u = 0; u < 5; ++u) cap[u] = ptx::f32x2(a.cap_c[u], a.cap_c[u]);
+    }
+    int cq = 0;  // Q copies so far
+    // Q of a part into TMEM Q_{cq&1}, hi and lo; returns my row's exponent.
+    // Warp w copies half w/4 of the elements of rows 32*(w%4) + lane.
+    int eq_new = 0;
+    auto copy_q = [&](const CachePart& p) -> bool {
+      const int c = cq & 1;
+      const int rows = min(128, a.R - p.rt * 128);
+      const int qr = quad * 32 + lane;
+      uint4 x[D / 8];
+      uint32_t mx = 0;
+      if (quad * 32 < rows) {
+        const int rr = p.rt * 128 + qr;
+        const int hg = rr / a.B, tb = rr - hg * a.B;
+        const uint16_t* src = a.q + p.n * a.qs_n + (static_cast<size_t>(p.hk) * a.group + hg) * a.qs_h + tb * a.qs_b;
+#pragma unroll
+        for (int u = 0; u < D / 8; ++u)
+          x[u] = qr < rows ? *reinterpret_cast<const uint4*>(src + u * 8) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+        for (int u = 0; u < D / 8; ++u) {
+          const uint32_t w[4] = {x[u].x, x[u].y, x[u].z, x[u].w};
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const uint32_t lo = w[e] & 0x7FFFu, hi = (w[e] >> 16) & 0x7FFFu;
+            mx = max(mx, lo < 0x7F80u ? lo : 0u);
+            mx = max(mx, hi < 0x7F80u ? hi : 0u);
+          }
+        }
+      }
+      const int e = exponent_for(mx);
+      if (cq >= 2 &&
+          !ptx::mbar_wait_warp(bar(C::B_QTEMPTY + c), ((cq >> 1) - 1) & 1, abort_flag, a.timeout_ns, kErrTimeout))
+        return false;
+      ptx::tc_fence_after();
+      if (quad * 32 < rows) {
+        const float inv = pow2i(-e);
+        uint32_t hi4[D / 8], lo4[D / 8];  // my half: D/2 elements, four to a word
+#pragma unroll
+        for (int u = 0; u < D / 16; ++u) {
+          const uint4 v = hw ? x[D / 16 + u] : x[u];
+          float f[8];
+          bf16x8_to_f32(v, f);
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
+            f[k] *= inv;
+            if (fabsf(f[k]) == __int_as_float(0x7f800000)) f[k] = __int_as_float(0x7fffffff);  // inf has no e4m3
+          }
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            const uint32_t h0 = pack_e4m3x2(f[4 * k], f[4 * k + 1]), h1 = pack_e4m3x2(f[4 * k + 2], f[4 * k + 3]);
+            float g0, g1, g2, g3;
+            unpack_e4m3x2(h0, g0, g1);
+            unpack_e4m3x2(h1, g2, g3);
+            hi4[2 * u + k] = h0 | (h1 << 16);
+            lo4[2 * u + k] = pack_e4m3x2(f[4 * k] - g0, f[4 * k + 1] - g1) |
+                             (pack_e4m3x2(f[4 * k + 2] - g2, f[4 * k + 3] - g3) << 16);
+          }
+        }
+        const uint32_t qa = tmem + (static_cast<uint32_t>(quad * 32) << 16) + (c ? C::TM_Q1 : C::TM_Q0) + hw * (D / 8);
+        if constexpr (D == 128) {
+          ptx::tmem_st32_16(qa, hi4);
+          ptx::tmem_st32_16(qa + D / 4, lo4);
+        } else {
+          ptx::tmem_st32_8(qa, hi4);
+          ptx::tmem_st32_8(qa + D / 4, lo4);
+        }
+        ptx::tmem_wait_st();
+      }
+      ptx::tc_fence_before();
+      eq_new = __shfl_sync(0xffffffffu, e, hw * 16 + (lane & 15));
+      __syncwarp();
+      if (lane == 0) ptx::mbar_arrive(bar(C::B_QTFULL + c));
+      ++cq;
+      return true;
+    };
+    int g = 0;
+    bool ok = true;
+    CachePart nextp;
+    bool have = run.next(a, &nextp);
+    if (have && !copy_q(nextp)) ok = false;
+    while (ok && have) {
+      part = nextp;
+      const int rows = min(128, a.R - part.rt * 128);
+      const bool warp_on = quad * 32 + hw * 16 < rows;
+      const bool row_valid = r < rows;
+      const long sbase = (static_cast<long>(part.n) * a.Hkv + part.hk) * (a.C / kCacheBlock);
+      const float qmul = pow2i(eq_new);
+      float slope2 = 0.f;
+      int at = 0;
+      if constexpr (MOD) {
+        const int rr = min(part.rt * 128 + r, a.R - 1);
+        const int hg = rr / a.B;
+        if (a.slopes) slope2 = a.slopes[part.hk * a.group + hg] * 1.44269504088896340736f;
+        at = (a.q_start ? min(max(a.q_start[part.n], -(1 << 29)), 1 << 29) : part.len - a.B) + (rr - hg * a.B);
+      }
+      float m = ninf, l = 0.f;
+      auto scale_of = [&](int t) -> float {
+        const int blk = min(2 * t + half, a.C / kCacheBlock - 1);
+        return warp_on ? a.k_scale[sbase + blk] : 1.f;
+      };
+      float ks_next = scale_of(part.t0);
+      const int vref = part_vref(a, part, lane);
+      for (int jj = 0; jj < part.cnt; ++jj, ++g) {
+        const int t = part.t0 + jj, b = g & 1;
+        const float ks = ks_next;
+        if (jj + 1 < part.cnt) ks_next = scale_of(t + 1);
+        if (!ptx::mbar_wait_warp(bar(C::B_SFULL + b), (g >> 1) & 1, abort_flag, a.timeout_ns, kErrTimeout)) {
+          ok = false;
+          break;
+        }
+        ptx::tc_fence_after();
+        if (warp_on) {
+          float s[HALF];
+          {
+            uint32_t raw[2][32];
+#pragma unroll
+            for (int c = 0; c < 2; ++c) ptx::tmem_ld16x2_32<HALF>(lane_base + (b ? C::TM_S1 : C::TM_S0) + c * 32, raw[c]);
+            ptx::tmem_wait_ld();
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+              ptx::reg_fence32(raw[c]);
+#pragma unroll
+              for (int e = 0; e < 32; ++e) s[c * 32 + e] = __uint_as_float(raw[c][e]);
+            }
+          }
+          // <q, k> from the scaled operands; the factor stays finite
+          const float f2 = fminf(qmul * pow2i(scale_exponent(ks)), 1e37f);
+          float f = fminf(f2 * a.scale_log2, 1e37f);
+          const int valid = part.len - t * C::BK - half * HALF;
+          if constexpr (MOD) {
+            f = 1.f;
+            if (valid < HALF) {  // what lies past the length has no say in the path taken
+#pragma unroll
+              for (int c = 0; c < HALF; ++c)
+                if (c >= valid) s[c] = 0.f;
+            }
+            if (a.capped) {
+              const uint64_t f22 = ptx::f32x2(f2, f2);
+#pragma unroll
+              for (int c = 0; c < HALF; c += 2)
+                ptx::f32x2_split(mul_f32x2(ptx::f32x2(s[c], s[c + 1]), f22), s[c], s[c + 1]);
+              const bool wide = __any_sync(0xffffffffu, fmaxf(row_max(s), -row_min(s)) > a.cap_fast);
+              if (wide) {
+#pragma unroll
+                for (int c = 0; c < HALF; ++c) s[c] = a.cap_log2 * tanh_wide(s[c] * a.cap_in);
+              } else {
+#pragma unroll
+                for (int c = 0; c < HALF; c += 2) {
+                  const uint64_t v = ptx::f32x2(s[c], s[c + 1]);
+                  ptx::f32x2_split(mul_f32x2(v, cap_poly(v, cap)), s[c], s[c + 1]);
+                }
+              }
+            } else {
+              const float ff = fminf(f2 * a.scale_log2, 1e37f);
+              const uint64_t f22 = ptx::f32x2(ff, ff);
+#pragma unroll
+              for (int c = 0; c < HALF; c += 2)
+                ptx::f32x2_split(mul_f32x2(ptx::f32x2(s[c], s[c + 1]), f22), s[c], s[c + 1]);
+            }
+            if (a.slopes) {
+              // a thread's 64 keys against its own row: one side or around it
+              const int c0 = t * C::BK + half * HALF;
+              const bool around = __any_sync(0xffffffffu, at > c0 && at < c0 + HALF - 1);
+              if (around) add_bias(s, slope2, at, c0, 0);
+              else add_bias(s, slope2, at, c0, at <= c0 ? 1 : -1);
+            }
+          }
+          if (valid < HALF) {
+#pragma unroll
+            for (int c = 0; c < HALF; ++c)
+              if (c >= valid) s[c] = ninf;
+          }
+          float mx = row_max(s) * f;
+          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
+          const float m_new = fmaxf(m, mx);
+          if (jj == 0) {
+            m = m_new;
+          } else if (__any_sync(0xffffffffu, m_new > m + 8.0f)) {
+            if (!ptx::mbar_wait_warp(bar(C::B_PVDONE + ((g - 1) & 1)), ((g - 1) >> 1) & 1, abort_flag, a.timeout_ns,
+                                     kErrTimeout)) {
+              ok = false;
+              break;
+            }
+            ptx::tc_fence_after();
+            const float alpha = m_new == ninf ? 1.0f : ptx::ex2(m - m_new);
+#pragma unroll
+            for (int c = 0; c < D / 64; ++c) {
+              uint32_t raw[32];
+              ptx::tmem_ld16x2_32<D / 2>(lane_base + C::TM_O + c * 32, raw);
+              ptx::tmem_wait_ld();
+              ptx::reg_fence32(raw);
+#pragma unroll
+              for (int e = 0; e < 32; ++e) raw[e] = __float_as_uint(__uint_as_float(raw[e]) * alpha);
+              ptx::tmem_st16x2_32<D / 2>(lane_base + C::TM_O + c * 32, raw);
+            }
+            ptx::tmem_wait_st();
+            l *= alpha;
+            m = m_new;
+          }
+          const float neg = (m == ninf ? 0.f : -m) + kPShift;
+          const uint64_t f2x = ptx::f32x2(f, f), neg2 = ptx::f32x2(neg, neg);
+          uint64_t acc0 = ptx::f32x2(0.f, 0.f), acc1 = acc0;
+          uint32_t pk[32];
+#pragma unroll
+          for (int e = 0; e < HALF / 2; ++e) {
+            float x0, x1;
+            ptx::f32x2_split(ptx::fma_f32x2(ptx::f32x2(s[2 * e], s[2 * e + 1]), f2x, neg2), x0, x1);
+            const float p0 = ptx::ex2(x0), p1 = ptx::ex2(x1);
+            if (e & 1) acc1 = ptx::add_f32x2(acc1, ptx::f32x2(p0, p1));
+            else acc0 = ptx::add_f32x2(acc0, ptx::f32x2(p0, p1));
+            pk[e] = ptx::pack_f16x2(p0, p1);
+          }
+          ptx::tmem_st16x2_32<HALF / 2>(lane_base + (b ? C::TM_S1 : C::TM_S0), pk);
+          float a0, a1, b0, b1;
+          ptx::f32x2_split(acc0, a0, a1);
+          ptx::f32x2_split(acc1, b0, b1);
+          l += (a0 + b0) + (a1 + b1);
+          ptx::tmem_wait_st();
+        }
+        ptx::tc_fence_before();
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(bar(C::B_PFULL + b));
+      }
+      if (!ok) break;
+      have = run.next(a, &nextp);
+      // the next part's Q into TMEM now, so its S MMAs start during this epilogue
+      if (have && !copy_q(nextp)) {
+        ok = false;
+        break;
+      }
+      // ---- epilogue
+      if (!ptx::mbar_wait_warp(bar(C::B_PVDONE + ((g - 1) & 1)), ((g - 1) >> 1) & 1, abort_flag, a.timeout_ns,
+                               kErrTimeout)) {
+        ok = false;
+        break;
+      }
+      ptx::tc_fence_after();
+      if (warp_on) {
+        const float lt = l + __shfl_xor_sync(0xffffffffu, l, 16);
+        const bool empty = lt == 0.f;
+        const float f = (empty ? 0.f : 1.0f / lt) * pow2i(vref);
+        const float lse2 = empty ? ninf : m - kPShift + ptx::lg2(lt);
+        const bool whole = part.cnt == part.nt;
+        const long grow = (static_cast<long>(part.n) * a.Hkv + part.hk) * a.R + part.rt * 128 + r;
+        const long prow = static_cast<long>(2 * blockIdx.x + (part.t0 == 0 ? 1 : 0)) * a.part_rows + r;
+        uint4* o_dst = reinterpret_cast<uint4*>(a.o + grow * D) + half * (D / 16);
+        float4* p_dst = reinterpret_cast<float4*>(a.o_part + prow * D) + half * (D / 8);
+#pragma unroll
+        for (int c = 0; c < D / 64; ++c) {
+          uint32_t raw[32];
+          ptx::tmem_ld16x2_32<D / 2>(lane_base + C::TM_O + c * 32, raw);
+          ptx::tmem_wait_ld();
+          ptx::reg_fence32(raw);
+          float v[32];
+#pragma unroll
+          for (int e = 0; e < 32; ++e) v[e] = empty ? 0.f : __uint_as_float(raw[e]) * f;
+          if (row_valid) {
+            if (whole) {
+#pragma unroll
+              for (int u = 0; u < 4; ++u)
+                o_dst[c * 4 + u] = make_uint4(ptx::pack_bf16x2(v[8 * u], v[8 * u + 1]), ptx::pack_bf16x2(v[8 * u + 2], v[8 * u + 3]),
+                                              ptx::pack_bf16x2(v[8 * u + 4], v[8 * u + 5]), ptx::pack_bf16x2(v[8 * u + 6], v[8 * u + 7]));
+            } else {
+#pragma unroll
+              for (int u = 0; u < 8; ++u) p_dst[c * 8 + u] = make_float4(v[4 * u], v[4 * u + 1], v[4 * u + 2], v[4 * u + 3]);
+            }
+          }
+        }
+        if (row_valid && half == 0) {
+          if (whole) a.lse[grow] = lse2 * 0.69314718055994530942f;
+          else a.l_part[prow] = lse2;
+        }
+      }
+      // the next part's first PV overwrites O only after this warp's next PFULL
+      // arrival, which follows the loads above
+    }
+  }
+
+  ptx::tc_fence_before();
+  __syncthreads();
+  if (warp == 9) {
+    ptx::tc_fence_after();
+    ptx::tmem_dealloc(tmem, C::TM_ALLOC);
+  }
+}
+
+// Joins the partial results of items cut by the ends of runs:
+//   O = sum_i 2^(l_i - L) O_i,  L = log2 sum_i 2^(l_i)
+// in the order of the runs, and writes the rows of empty sequences. One CTA per
+// item (blockIdx.y: sequence, blockIdx.x: its kv head and row tile); a warp
+// takes whole rows. `runs`: the CTAs of the attention kernel.
+template <int D>
+__global__ void __launch_bounds__(128) cache_merge_kernel(const __grid_constant__ CacheArgs a, int runs) {
+  constexpr int V = D / 32;  // elements of a lane
+  ptx::grid_dep_wait();
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const float ninf = -__int_as_float(0x7f800000);
+  const int n = blockIdx.y, item = blockIdx.x;
+  const int hk = item / a.RT, rt = item - hk * a.RT;
+  const int rows = min(128, a.R - rt * 128);
+  const long grow0 = (static_cast<long>(n) * a.Hkv + hk) * a.R + rt * 128;
+  const int nt = cache_tiles(cache_len(a, n));
+  if (nt == 0) {
+    for (int r = warp; r < rows; r += 4) {
+      for (int e = lane; e < D; e += 32) a.o[(grow0 + r) * D + e] = 0;
+      if (lane == 0) a.lse[grow0 + r] = ninf;
+    }
+    return;
+  }
+  long before;
+  const long T = cache_total(a, lane, n, &before);
+  const long x0 = before + static_cast<long>(item) * nt, x1 = x0 + nt - 1;  // the item's tiles
+  // the runs that hold its first and last tile
+  int c0 = static_cast<int>(min(static_cast<long>(runs) - 1, x0 / max(1l, T / runs + 1)));
+  while (run_begin(T, c0 + 1, runs) <= x0) ++c0;
+  int c1 = c0;
+  while (run_begin(T, c1 + 1, runs) <= x1) ++c1;
+  if (c0 == c1) return;  // whole in one run: written there
+  for (int r = warp; r < rows; r += 4) {
+    float L = ninf;
+    for (int c = c0 + lane; c <= c1; c += 32)
+      if (run_begin(T, c, runs) < run_begin(T, c + 1, runs))
+        L = fmaxf(L, a.l_part[static_cast<long>(2 * c + (c == c0 ? 1 : 0)) * a.part_rows + r]);
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) L = fmaxf(L, __shfl_xor_sync(0xffffffffu, L, off));
+    const float base = L == ninf ? 0.f : L;
+    float sum = 0.f, acc[V];
+#pragma unroll
+    for (int e = 0; e < V; ++e) acc[e] = 0.f;
+#pragma unroll 4
+    for (int c = c0; c <= c1; ++c) {
+      if (run_begin(T, c, runs) == run_begin(T, c + 1, runs)) continue;  // an empty run
+      const long prow = static_cast<long>(2 * c + (c == c0 ? 1 : 0)) * a.part_rows + r;
+      const float w = ptx::ex2(a.l_part[prow] - base);
+      sum += w;
+      const float* src = a.o_part + prow * D + lane * V;
+#pragma unroll
+      for (int e = 0; e < V; ++e) acc[e] += w * src[e];
+    }
+    const float inv = sum == 0.f ? 0.f : 1.0f / sum;
+    uint32_t* dst = reinterpret_cast<uint32_t*>(a.o + (grow0 + r) * D) + lane * (V / 2);
+#pragma unroll
+    for (int e = 0; e < V / 2; ++e) dst[e] = ptx::pack_bf16x2(acc[2 * e] * inv, acc[2 * e + 1] * inv);
+    if (lane == 0) a.lse[grow0 + r] = sum == 0.f ? ninf : (base + ptx::lg2(sum)) * 0.69314718055994530942f;
+  }
+}
+
+}  // namespace sparsed

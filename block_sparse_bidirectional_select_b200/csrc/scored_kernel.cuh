@@ -720,4 +720,33 @@ __global__ void __launch_bounds__(384, 1)
   }
 }
 
+// Visible keys of every token of packed documents. starts [n_docs + 1]
+// ascending; token r of document i (starts[i] <= r < starts[i+1]) sees its
+// document's keys: all of them, or, with prefix [n_docs], the first prefix[i]
+// and those up to its own. Tokens of no document see nothing.
+__global__ void __launch_bounds__(256)
+    document_ranges_kernel(const int32_t* starts, const int32_t* prefix, int n_docs, int L, int2* ranges) {
+  const int r = blockIdx.x * 256 + threadIdx.x;
+  if (r >= L) return;
+  // the last document that starts at or before r
+  int lo = 0, hi = n_docs;
+  while (lo < hi) {
+    const int mid = (lo + hi) >> 1;
+    if (starts[mid] <= r) lo = mid + 1;
+    else hi = mid;
+  }
+  int2 out = make_int2(0, 0);
+  if (lo > 0) {
+    const int a = starts[lo - 1], b = min(starts[lo], L);
+    if (r < b) {
+      out = make_int2(max(a, 0), b);
+      if (prefix) {
+        const long p = static_cast<long>(a) + max(prefix[lo - 1], 0);
+        out.y = static_cast<int>(min(static_cast<long>(b), max(p, static_cast<long>(r) + 1)));
+      }
+    }
+  }
+  ranges[r] = out;
+}
+
 }  // namespace sparsed

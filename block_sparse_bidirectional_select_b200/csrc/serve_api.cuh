@@ -109,6 +109,66 @@ void cap_coefficients(float scale, float softcap, float (&c)[5], float* fast, fl
   *fast = !finite ? -1.f : (u > 0 && 0.6 / u < 1e18 ? static_cast<float>(0.6 / u) : 1e18f);
 }
 
+// Partial results of cache_attn: two slots per CTA.
+struct CachePartLayout {
+  int rows;
+  size_t lse, total;
+};
+CachePartLayout cache_part_layout(int B, int group, int d) {
+  CachePartLayout w;
+  const long rows = static_cast<long>(B) * group;
+  w.rows = static_cast<int>(rows < 1 ? 1 : (rows < 128 ? rows : 128));
+  w.lse = align256(static_cast<size_t>(2 * kCacheMaxCtas) * w.rows * d * sizeof(float));
+  w.total = w.lse + align256(static_cast<size_t>(2 * kCacheMaxCtas) * w.rows * sizeof(float));
+  return w;
+}
+
+// e4m3 [H, C, d] as a 3-D tensor map, boxes of whole rows.
+int make_map_cache(CUtensorMap* m, const uint8_t* ptr, long H, int C, int d, CUtensorMapSwizzle swizzle) {
+  cuuint64_t dims[3] = {static_cast<cuuint64_t>(d), static_cast<cuuint64_t>(C), static_cast<cuuint64_t>(H)};
+  cuuint64_t strides[2] = {static_cast<cuuint64_t>(d), static_cast<cuuint64_t>(C) * d};
+  cuuint32_t box[3] = {static_cast<cuuint32_t>(d), kCacheTile, 1};
+  cuuint32_t es[3] = {1, 1, 1};
+  CUresult r = g_encode(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<uint8_t*>(ptr), dims, strides, box, es,
+                        CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                        CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS) return fail_cuda(cudaErrorInvalidValue);
+  return SPARSED_OK;
+}
+
+template <int D, bool MOD>
+int launch_cache_attn(const uint8_t* k8, const uint8_t* v8, const CacheArgs& a, cudaStream_t st) {
+  using C = CacheCfg<D>;
+  const unsigned items = static_cast<unsigned>(a.Hkv) * static_cast<unsigned>(a.RT);
+  int sms = 0;
+  SP_TRY(sm_count(&sms));
+  if (sms > kCacheMaxCtas) sms = kCacheMaxCtas;
+  // no more runs than there can be key tiles
+  const long most = static_cast<long>(a.N) * items * cdiv(a.C, kCacheTile);
+  const int runs = static_cast<int>(most < sms ? most : sms);
+  if (runs > 0) {
+    auto kern = cache_attn_kernel<D, MOD>;
+    // the register split must be funded by the launch (as launch_attn_t)
+    static int regs = -1;
+    if (regs < 0) {
+      cudaFuncAttributes fa;
+      SP_CUDA(cudaFuncGetAttributes(&fa, kern));
+      regs = fa.numRegs;
+    }
+    if (regs * C::THREADS < C::REGS_SOFTMAX * 256 + C::REGS_CONTROL * 128 + C::REGS_WIDEN * 128)
+      return SPARSED_ERR_UNSUPPORTED;
+    CUtensorMap tk, tv;
+    const long H = static_cast<long>(a.N) * a.Hkv;
+    SP_TRY(make_map_cache(&tk, k8, H, a.C, D, D == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B));
+    SP_TRY(make_map_cache(&tv, v8, H, a.C, D, CU_TENSOR_MAP_SWIZZLE_NONE));
+    SP_CUDA(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM_BYTES));
+    kern<<<runs, C::THREADS, C::SMEM_BYTES, st>>>(tk, tv, a);
+    SP_CUDA(cudaGetLastError());
+  }
+  return launch_k(cache_merge_kernel<D>, dim3(items, static_cast<unsigned>(a.N)), dim3(128), 0, st, runs > 0, a,
+                  runs > 0 ? runs : 1);
+}
+
 }  // namespace
 
 extern "C" {
@@ -215,7 +275,7 @@ int sparsed_cache_append(const uint16_t* K, size_t k_stride_n, size_t k_stride_h
 int sparsed_cache_attn_workspace_bytes(int N, int Hq, int Hkv, int B, int d, size_t* bytes) {
   if (!bytes || N < 0 || Hq < 0 || Hkv < 0 || B < 0) return SPARSED_ERR_INVALID_ARG;
   if (d != 64 && d != 128) return SPARSED_ERR_UNSUPPORTED;
-  *bytes = 256;
+  *bytes = cache_part_layout(B, Hkv > 0 ? Hq / Hkv : 0, d).total;
   return SPARSED_OK;
 }
 
@@ -230,41 +290,51 @@ int sparsed_cache_attn(const uint16_t* Q, size_t q_stride_n, size_t q_stride_h, 
   if (d != 64 && d != 128) return SPARSED_ERR_UNSUPPORTED;
   if (N == 0 || Hq == 0 || B == 0) return SPARSED_OK;
   if (Hkv == 0 || Hq % Hkv != 0) return SPARSED_ERR_INVALID_ARG;
-  if (N > 65535 || Hq > 65535 || C > (1 << 30)) return SPARSED_ERR_UNSUPPORTED;
-  if (!Q || !k8 || !v8 || !k_scale || !v_scale || !lengths || !O || !LSE) return SPARSED_ERR_INVALID_ARG;
+  if (N > 65535 || Hq > 65535 || C > (1 << 29) || B > (1 << 24)) return SPARSED_ERR_UNSUPPORTED;
+  if (!Q || !O || !LSE || !lengths || (C > 0 && (!k8 || !v8 || !k_scale || !v_scale))) return SPARSED_ERR_INVALID_ARG;
   if (!aligned16(Q) || !aligned16(k8) || !aligned16(v8) || !aligned16(O) || !aligned4(LSE) || !aligned4(lengths) ||
       !aligned4(q_start) || !aligned4(k_scale) || !aligned4(v_scale))
     return SPARSED_ERR_INVALID_ARG;
   if (((q_stride_n | q_stride_h | q_stride_b) & 7u) != 0) return SPARSED_ERR_INVALID_ARG;
-  size_t need = 0;
-  SP_TRY(sparsed_cache_attn_workspace_bytes(N, Hq, Hkv, B, d, &need));
-  if (!workspace || workspace_bytes < need || (reinterpret_cast<uintptr_t>(workspace) & 255u)) return SPARSED_ERR_WORKSPACE;
+  const CachePartLayout w = cache_part_layout(B, Hq / Hkv, d);
+  if (!workspace || workspace_bytes < w.total || (reinterpret_cast<uintptr_t>(workspace) & 255u)) return SPARSED_ERR_WORKSPACE;
   SP_TRY(require_sm100());
-  RowsArgs a = {};
+  SP_TRY(get_encoder());
+  CacheArgs a = {};
   a.q = Q;
   a.qs_n = q_stride_n;
   a.qs_h = q_stride_h;
   a.qs_b = q_stride_b;
-  a.k8 = k8;
-  a.v8 = v8;
   a.k_scale = k_scale;
   a.v_scale = v_scale;
-  a.N = N;
-  a.Hq = Hq;
-  a.Hkv = Hkv;
-  a.B = B;
-  a.Lk = C;
   a.lengths = lengths;
   a.q_start = q_start;
-  a.mod = ScoreMod{scale, softcap, slopes};
+  a.N = N;
+  a.Hkv = Hkv;
+  a.group = Hq / Hkv;
+  a.B = B;
+  a.C = C;
+  const long R = static_cast<long>(a.group) * B;
+  if (R >= (1l << 30)) return SPARSED_ERR_UNSUPPORTED;
+  a.R = static_cast<int>(R);
+  a.RT = static_cast<int>(cdiv(R, 128));
+  a.part_rows = w.rows;
+  a.scale_log2 = scale * 1.44269504088896340736f;
+  if (a.scale_log2 < 1.17549435e-38f) a.scale_log2 = 1.17549435e-38f;  // as scored_attn
+  a.slopes = slopes;
+  a.capped = softcap > 0.f;
+  if (a.capped) cap_coefficients(scale, softcap, a.cap_c, &a.cap_fast, &a.cap_in, &a.cap_log2);
   a.o = O;
   a.lse = LSE;
-  const dim3 grid(B, Hq, N);
+  a.o_part = static_cast<float*>(workspace);
+  a.l_part = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + w.lse);
+  a.timeout_ns = kWaitTimeoutNs;
+  const long items = static_cast<long>(Hkv) * a.RT;
+  if (items >= (1l << 31)) return SPARSED_ERR_UNSUPPORTED;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  if (d == 64) score_rows_kernel<64><<<grid, 128, 0, st>>>(a);
-  else score_rows_kernel<128><<<grid, 128, 0, st>>>(a);
-  SP_CUDA(cudaGetLastError());
-  return SPARSED_OK;
+  const bool mod = a.capped || a.slopes;
+  if (d == 64) return mod ? launch_cache_attn<64, true>(k8, v8, a, st) : launch_cache_attn<64, false>(k8, v8, a, st);
+  return mod ? launch_cache_attn<128, true>(k8, v8, a, st) : launch_cache_attn<128, false>(k8, v8, a, st);
 }
 
 int sparsed_document_ranges(const int32_t* starts, const int32_t* prefix, int n_docs, int L, int32_t* ranges,

@@ -22,8 +22,8 @@
 #include "losa_kernels.cuh"
 #include "rope_kernels.cuh"
 #include "cache_kernels.cuh"
-#include "score_rows_kernel.cuh"
 #include "scored_kernel.cuh"
+#include "cache_attn_kernel.cuh"
 
 using namespace sparsed;
 
