@@ -28,10 +28,18 @@
 // the run's part of the item (a power of two: exact, or below 2^-24 of that
 // scale), so O accumulates in one unit.
 //
+// Few rows. A row tile of at most 64 (32) rows is held 2 (4) times in the 128
+// lanes of the accumulators, and copy i takes the keys i*128/K .. of every tile:
+// its P is zero elsewhere, so each copy is a softmax of its own over its keys.
+// The tensor cores do the same work as for 128 rows; the softmax warps, whose
+// time per tile is a row's length and not the number of rows, get a half (a
+// quarter) each and run on all four schedulers. The copies are joined through
+// shared memory when an item's part ends.
+//
 // Warp roles (512 threads):
-//   warps 0-7   softmax: warp w covers rows 32*(w%4) + 16*(w/4) + 0..15, thread t
-//               row t%16 and key half t/16 (one scale block) of every tile; they
-//               also bring each item's Q into TMEM as hi and lo
+//   warps 0-7   softmax: warp w covers the lanes 32*(w%4) + 16*(w/4) + 0..15, thread
+//               t lane t%16 and half t/16 of its copy's keys; they also bring each
+//               item's Q into TMEM as hi and lo
 //   warp 8      TMA producer: K and V tiles
 //   warp 9      TMEM owner; issues S
 //   warp 10     issues O += P V
@@ -74,15 +82,16 @@ struct CacheArgs {
 template <int D>
 struct CacheCfg {
   static constexpr int BK = kCacheTile;
-  static constexpr int HALF = 64;
   static constexpr int T8 = BK * D;           // bytes of an e4m3 tile
   static constexpr int T16 = 2 * T8;
-  static constexpr int KS = D == 128 ? 5 : 8;
+  static constexpr int KS = D == 128 ? 4 : 8;
   static constexpr int VS = KS;
   static constexpr int OFF_K = 0;
   static constexpr int OFF_V = OFF_K + KS * T8;
   static constexpr int OFF_W = OFF_V + VS * T8;  // widened V, 2 buffers
-  static constexpr int OFF_BAR = OFF_W + 2 * T16;
+  static constexpr int OFF_J = OFF_W + 2 * T16;  // joining copies: 8 warps x 16 lanes x 64 fp32, then (m, l) of each lane
+  static constexpr int J_BYTES = 8 * 16 * 64 * 4;
+  static constexpr int OFF_BAR = OFF_J + J_BYTES + 8 * 16 * 8;
   static constexpr int B_KFULL = 0;
   static constexpr int B_KEMPTY = B_KFULL + KS;
   static constexpr int B_VFULL = B_KEMPTY + KS;
@@ -94,7 +103,8 @@ struct CacheCfg {
   static constexpr int B_DRAIN = B_PVDONE + 2;   // [2]
   static constexpr int B_QTFULL = B_DRAIN + 2;   // [2] 8 softmax-warp arrivals
   static constexpr int B_QTEMPTY = B_QTFULL + 2; // [2]
-  static constexpr int NUM_BARS = B_QTEMPTY + 2;
+  static constexpr int B_JOIN = B_QTEMPTY + 2;   // 8 softmax-warp arrivals
+  static constexpr int NUM_BARS = B_JOIN + 1;
   static constexpr int OFF_MISC = OFF_BAR + NUM_BARS * 8;  // tmem slot, abort flag, run
   static constexpr int SMEM_BYTES = OFF_MISC + 48 + 1024;
   static constexpr int TM_S0 = 0;
@@ -139,6 +149,40 @@ __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
   asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
   return r;
 }
+// "16x32bx2" accesses of 16, 8 and 4 columns per half (see tmem_ld16x2_32):
+// register i to or from column col + (t / 16) * SPLIT + i.
+template <int SPLIT>
+__device__ __forceinline__ void tmem_ld16x2(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.16x32bx2.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16], %17;"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr), "n"(SPLIT)
+      : "memory");
+}
+template <int SPLIT>
+__device__ __forceinline__ void tmem_st16x2(uint32_t taddr, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.16x32bx2.x16.b32 [%0], %17, {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "n"(SPLIT)
+      : "memory");
+}
+template <int SPLIT>
+__device__ __forceinline__ void tmem_st16x2(uint32_t taddr, const uint32_t (&r)[8]) {
+  asm volatile("tcgen05.st.sync.aligned.16x32bx2.x8.b32 [%0], %9, {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr), "r"(r[0]),
+               "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "n"(SPLIT)
+               : "memory");
+}
+template <int SPLIT>
+__device__ __forceinline__ void tmem_st16x2(uint32_t taddr, const uint32_t (&r)[32]) {
+  tmem_st16x2_32<SPLIT>(taddr, r);
+}
+// Keeps uses of r below a preceding tmem_wait_ld (as reg_fence32).
+__device__ __forceinline__ void reg_fence16(uint32_t (&r)[16]) {
+  asm volatile("" : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+               "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]));
+}
 __device__ __forceinline__ void setmaxnreg_inc_184() { asm volatile("setmaxnreg.inc.sync.aligned.u32 184;" ::: "memory"); }
 __device__ __forceinline__ void setmaxnreg_dec_88() { asm volatile("setmaxnreg.dec.sync.aligned.u32 88;" ::: "memory"); }
 }  // namespace ptx
@@ -165,8 +209,8 @@ __device__ __forceinline__ long cache_total(const CacheArgs& a, int lane, int n_
 
 // First tile of run c of G runs over T tiles.
 __device__ __forceinline__ long run_begin(long T, int c, int G) {
-  const long q = T / G, r = T - q * G;
-  return q * c + (r * c) / G;
+  const long q = T / G;
+  return q * c + static_cast<int>(T - q * G) * c / G;
 }
 
 // A run's parts: the tiles of one item that lie in it.
@@ -214,12 +258,39 @@ __device__ __forceinline__ int part_vref(const CacheArgs& a, const CachePart& p,
   return __reduce_max_sync(0xffffffffu, e);
 }
 
-template <int D, bool MOD>
+// N scores of a thread (64, 32 or 16) from its lane of S: N columns from
+// `taddr` for half 0, N further on for half 1.
+template <int N>
+__device__ __forceinline__ void load_scores(uint32_t taddr, float (&s)[N]) {
+  if constexpr (N == 16) {
+    uint32_t raw[16];
+    ptx::tmem_ld16x2<16>(taddr, raw);
+    ptx::tmem_wait_ld();
+    ptx::reg_fence16(raw);
+#pragma unroll
+    for (int e = 0; e < 16; ++e) s[e] = __uint_as_float(raw[e]);
+  } else {
+    uint32_t raw[N / 32][32];
+#pragma unroll
+    for (int c = 0; c < N / 32; ++c) ptx::tmem_ld16x2_32<N>(taddr + c * 32, raw[c]);
+    ptx::tmem_wait_ld();
+#pragma unroll
+    for (int c = 0; c < N / 32; ++c) {
+      ptx::reg_fence32(raw[c]);
+#pragma unroll
+      for (int e = 0; e < 32; ++e) s[c * 32 + e] = __uint_as_float(raw[c][e]);
+    }
+  }
+}
+
+// K: copies of a row tile in the accumulators' lanes (1, 2 or 4).
+template <int D, bool MOD, int K>
 __global__ void __launch_bounds__(512, 1)
     cache_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                       const __grid_constant__ CacheArgs a) {
   using C = CacheCfg<D>;
-  constexpr int HALF = C::HALF;
+  constexpr int COLS = C::BK / K;  // keys of a copy in a tile
+  constexpr int N = COLS / 2;      // keys of a thread
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~static_cast<uintptr_t>(1023));
@@ -248,6 +319,7 @@ __global__ void __launch_bounds__(512, 1)
       ptx::mbar_init(bar(C::B_QTFULL + b), 8);
       ptx::mbar_init(bar(C::B_QTEMPTY + b), 1);
     }
+    ptx::mbar_init(bar(C::B_JOIN), 8);
     *abort_flag = 0;
     ptx::fence_mbar_init();
   }
@@ -306,25 +378,37 @@ __global__ void __launch_bounds__(512, 1)
     constexpr int NP = C::BK / ROWS;
     const int j = tid % TPR, row0 = tid / TPR;
     const int chunk = j >> 2;
-    // the two 16-byte units of a thread; odd chunks write the second first, so
-    // that eight threads of a row cover all banks
-    const int ua = 2 * (j & 3) + (chunk & 1), ub = ua ^ 1;
+    // The two 16-byte units of a thread's f16 values. With 128 elements a row,
+    // the threads of its second half write their second unit first, so that
+    // eight threads of a row cover all banks.
+    const bool sw = (chunk & 1) != 0;
+    const int swz = row0 & 7;  // ROWS is a multiple of 8
+    const uint32_t off_a = row0 * 128 + (((2 * (j & 3) + (sw ? 1 : 0)) ^ swz) << 4) + chunk * (C::BK * 128);
+    const uint32_t off_b = row0 * 128 + (((2 * (j & 3) + (sw ? 0 : 1)) ^ swz) << 4) + chunk * (C::BK * 128);
     int g = 0;
     bool ok = true;
     while (ok && run.next(a, &part)) {
       const int vref = part_vref(a, part, lane);
       const float* vs = a.v_scale + (static_cast<long>(part.n) * a.Hkv + part.hk) * (a.C / kCacheBlock);
+      const int last = a.C / kCacheBlock - 1;
+      // the next tile's scales are read a tile ahead
+      float sc0 = vs[2 * part.t0], sc1 = vs[min(2 * part.t0 + 1, last)];
       for (int t = part.t0; t < part.t0 + part.cnt; ++t, ++g) {
         const int st = g % C::VS, b = g & 1;
         const int valid = part.len - t * C::BK;
-        // 2^(ev - vref) of both scale blocks as f16 pairs
+        // 2^(ev - vref) of both scale blocks as f16 pairs (0 below f16's range,
+        // which includes a block past the length: its rows are cleared)
         uint32_t mul[2];
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
-          const int dlt = (x * kCacheBlock < valid ? scale_exponent(vs[2 * t + x]) : kCacheEMin) - vref;
+          const int dlt = min(scale_exponent(x ? sc1 : sc0) - vref, 0);
           const uint32_t hbits = dlt >= -14 ? static_cast<uint32_t>(dlt + 15) << 10
                                             : (dlt >= -24 ? 1u << (dlt + 24) : 0u);
           mul[x] = hbits | (hbits << 16);
+        }
+        if (t + 1 < part.t0 + part.cnt) {
+          sc0 = vs[2 * t + 2];
+          sc1 = vs[min(2 * t + 3, last)];
         }
         if (!ptx::mbar_wait_warp(bar(C::B_VFULL + st), (g / C::VS) & 1, abort_flag, a.timeout_ns, kErrTimeout) ||
             (g >= 2 &&
@@ -332,16 +416,20 @@ __global__ void __launch_bounds__(512, 1)
           ok = false;
           break;
         }
-        const uint8_t* src = smem + C::OFF_V + st * C::T8 + j * 16;
-        uint8_t* dst = smem + C::OFF_W + b * C::T16 + chunk * (C::BK * 128);
+        const uint8_t* src = smem + C::OFF_V + st * C::T8 + row0 * D + j * 16;
+        uint8_t* dst = smem + C::OFF_W + b * C::T16;
         uint4 x[NP];
 #pragma unroll
-        for (int p = 0; p < NP; ++p) x[p] = *reinterpret_cast<const uint4*>(src + (row0 + p * ROWS) * D);
+        for (int p = 0; p < NP; ++p) x[p] = *reinterpret_cast<const uint4*>(src + p * (ROWS * D));
+        if (valid < C::BK) {
+#pragma unroll
+          for (int p = 0; p < NP; ++p)
+            if (row0 + p * ROWS >= valid) x[p] = make_uint4(0, 0, 0, 0);
+        }
 #pragma unroll
         for (int p = 0; p < NP; ++p) {
-          const int row = row0 + p * ROWS;
-          const uint32_t w[4] = {x[p].x, x[p].y, x[p].z, x[p].w};
           const uint32_t m2 = mul[p >= NP / 2 ? 1 : 0];
+          const uint32_t w[4] = {sw ? x[p].z : x[p].x, sw ? x[p].w : x[p].y, sw ? x[p].x : x[p].z, sw ? x[p].y : x[p].w};
           uint32_t h[8];
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
@@ -352,16 +440,8 @@ __global__ void __launch_bounds__(512, 1)
             asm("mul.rn.f16x2 %0, %0, %1;" : "+r"(h[2 * e]) : "r"(m2));
             asm("mul.rn.f16x2 %0, %0, %1;" : "+r"(h[2 * e + 1]) : "r"(m2));
           }
-          if (row >= valid) {
-#pragma unroll
-            for (int e = 0; e < 8; ++e) h[e] = 0u;
-          }
-          const bool sw = (chunk & 1) != 0;
-          uint8_t* rp = dst + row * 128;
-          *reinterpret_cast<uint4*>(rp + ((ua ^ (row & 7)) << 4)) =
-              make_uint4(sw ? h[4] : h[0], sw ? h[5] : h[1], sw ? h[6] : h[2], sw ? h[7] : h[3]);
-          *reinterpret_cast<uint4*>(rp + ((ub ^ (row & 7)) << 4)) =
-              make_uint4(sw ? h[0] : h[4], sw ? h[1] : h[5], sw ? h[2] : h[6], sw ? h[3] : h[7]);
+          *reinterpret_cast<uint4*>(dst + off_a + p * (ROWS * 128)) = make_uint4(h[0], h[1], h[2], h[3]);
+          *reinterpret_cast<uint4*>(dst + off_b + p * (ROWS * 128)) = make_uint4(h[4], h[5], h[6], h[7]);
         }
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         __syncwarp();
@@ -490,7 +570,12 @@ __global__ void __launch_bounds__(512, 1)
     ptx::setmaxnreg_inc_184();
     const int half = lane >> 4;
     const int quad = warp & 3, hw = warp >> 2;
-    const int r = quad * 32 + hw * 16 + (lane & 15);  // row == TMEM lane
+    // lanes 16*hw.. of a quad hold the 16 rows of block rb for copy `copy`
+    const int copy = K == 1 ? 0 : (K == 2 ? hw : quad);
+    const int rb = K == 1 ? 2 * quad + hw : (K == 2 ? quad : hw);
+    const int r = rb * 16 + (lane & 15);           // my row
+    const int key0 = copy * COLS + half * N;       // my first key of a tile
+    const int sblk = key0 / kCacheBlock;           // ... its scale block
     const uint32_t lane_base = tmem + (static_cast<uint32_t>(quad * 32 + hw * 16) << 16);
     const float ninf = -__int_as_float(0x7f800000);
     uint64_t cap[5];
@@ -500,24 +585,24 @@ __global__ void __launch_bounds__(512, 1)
     }
     int cq = 0;  // Q copies so far
     // Q of a part into TMEM Q_{cq&1}, hi and lo; returns my row's exponent.
-    // Warp w copies half w/4 of the elements of rows 32*(w%4) + lane.
+    // Warp w copies half w/4 of the elements of the rows in lanes 32*(w%4) + lane.
     int eq_new = 0;
     auto copy_q = [&](const CachePart& p) -> bool {
       const int c = cq & 1;
       const int rows = min(128, a.R - p.rt * 128);
-      const int qr = quad * 32 + lane;
-      uint4 x[D / 8];
+      const int qr = K == 1 ? quad * 32 + lane : (K == 2 ? quad * 16 + (lane & 15) : lane);
       uint32_t mx = 0;
-      if (quad * 32 < rows) {
-        const int rr = p.rt * 128 + qr;
+      const uint16_t* src = nullptr;
+      const bool quad_on = __any_sync(0xffffffffu, qr < rows);
+      if (quad_on) {
+        const int rr = p.rt * 128 + min(qr, rows - 1);
         const int hg = rr / a.B, tb = rr - hg * a.B;
-        const uint16_t* src = a.q + p.n * a.qs_n + (static_cast<size_t>(p.hk) * a.group + hg) * a.qs_h + tb * a.qs_b;
-#pragma unroll
-        for (int u = 0; u < D / 8; ++u)
-          x[u] = qr < rows ? *reinterpret_cast<const uint4*>(src + u * 8) : make_uint4(0, 0, 0, 0);
-#pragma unroll
+        src = a.q + p.n * a.qs_n + (static_cast<size_t>(p.hk) * a.group + hg) * a.qs_h + tb * a.qs_b;
+        // the whole row for its maximum; my half is read again below (from L1)
+#pragma unroll 8
         for (int u = 0; u < D / 8; ++u) {
-          const uint32_t w[4] = {x[u].x, x[u].y, x[u].z, x[u].w};
+          const uint4 x = qr < rows ? *reinterpret_cast<const uint4*>(src + u * 8) : make_uint4(0, 0, 0, 0);
+          const uint32_t w[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
             const uint32_t lo = w[e] & 0x7FFFu, hi = (w[e] >> 16) & 0x7FFFu;
@@ -531,12 +616,13 @@ __global__ void __launch_bounds__(512, 1)
           !ptx::mbar_wait_warp(bar(C::B_QTEMPTY + c), ((cq >> 1) - 1) & 1, abort_flag, a.timeout_ns, kErrTimeout))
         return false;
       ptx::tc_fence_after();
-      if (quad * 32 < rows) {
+      if (quad_on) {
         const float inv = pow2i(-e);
         uint32_t hi4[D / 8], lo4[D / 8];  // my half: D/2 elements, four to a word
 #pragma unroll
         for (int u = 0; u < D / 16; ++u) {
-          const uint4 v = hw ? x[D / 16 + u] : x[u];
+          const uint4 v =
+              qr < rows ? *reinterpret_cast<const uint4*>(src + hw * (D / 2) + u * 8) : make_uint4(0, 0, 0, 0);
           float f[8];
           bf16x8_to_f32(v, f);
 #pragma unroll
@@ -573,14 +659,21 @@ __global__ void __launch_bounds__(512, 1)
       return true;
     };
     int g = 0;
+    int joins = 0;  // phases of B_JOIN
     bool ok = true;
+    // every softmax warp has come here (K > 1: copies exchange through shared memory)
+    auto join = [&]() -> bool {
+      __syncwarp();
+      if (lane == 0) ptx::mbar_arrive(bar(C::B_JOIN));
+      return ptx::mbar_wait_warp(bar(C::B_JOIN), joins++ & 1, abort_flag, a.timeout_ns, kErrTimeout);
+    };
     CachePart nextp;
     bool have = run.next(a, &nextp);
     if (have && !copy_q(nextp)) ok = false;
     while (ok && have) {
       part = nextp;
       const int rows = min(128, a.R - part.rt * 128);
-      const bool warp_on = quad * 32 + hw * 16 < rows;
+      const bool warp_on = rb * 16 < rows;
       const bool row_valid = r < rows;
       const long sbase = (static_cast<long>(part.n) * a.Hkv + part.hk) * (a.C / kCacheBlock);
       const float qmul = pow2i(eq_new);
@@ -594,7 +687,7 @@ __global__ void __launch_bounds__(512, 1)
       }
       float m = ninf, l = 0.f;
       auto scale_of = [&](int t) -> float {
-        const int blk = min(2 * t + half, a.C / kCacheBlock - 1);
+        const int blk = min(2 * t + sblk, a.C / kCacheBlock - 1);
         return warp_on ? a.k_scale[sbase + blk] : 1.f;
       };
       float ks_next = scale_of(part.t0);
@@ -609,42 +702,31 @@ __global__ void __launch_bounds__(512, 1)
         }
         ptx::tc_fence_after();
         if (warp_on) {
-          float s[HALF];
-          {
-            uint32_t raw[2][32];
-#pragma unroll
-            for (int c = 0; c < 2; ++c) ptx::tmem_ld16x2_32<HALF>(lane_base + (b ? C::TM_S1 : C::TM_S0) + c * 32, raw[c]);
-            ptx::tmem_wait_ld();
-#pragma unroll
-            for (int c = 0; c < 2; ++c) {
-              ptx::reg_fence32(raw[c]);
-#pragma unroll
-              for (int e = 0; e < 32; ++e) s[c * 32 + e] = __uint_as_float(raw[c][e]);
-            }
-          }
+          float s[N];
+          load_scores<N>(lane_base + (b ? C::TM_S1 : C::TM_S0) + copy * COLS, s);
           // <q, k> from the scaled operands; the factor stays finite
           const float f2 = fminf(qmul * pow2i(scale_exponent(ks)), 1e37f);
           float f = fminf(f2 * a.scale_log2, 1e37f);
-          const int valid = part.len - t * C::BK - half * HALF;
+          const int valid = part.len - t * C::BK - key0;
           if constexpr (MOD) {
             f = 1.f;
-            if (valid < HALF) {  // what lies past the length has no say in the path taken
+            if (valid < N) {  // what lies past the length has no say in the path taken
 #pragma unroll
-              for (int c = 0; c < HALF; ++c)
+              for (int c = 0; c < N; ++c)
                 if (c >= valid) s[c] = 0.f;
             }
             if (a.capped) {
               const uint64_t f22 = ptx::f32x2(f2, f2);
 #pragma unroll
-              for (int c = 0; c < HALF; c += 2)
+              for (int c = 0; c < N; c += 2)
                 ptx::f32x2_split(mul_f32x2(ptx::f32x2(s[c], s[c + 1]), f22), s[c], s[c + 1]);
               const bool wide = __any_sync(0xffffffffu, fmaxf(row_max(s), -row_min(s)) > a.cap_fast);
               if (wide) {
 #pragma unroll
-                for (int c = 0; c < HALF; ++c) s[c] = a.cap_log2 * tanh_wide(s[c] * a.cap_in);
+                for (int c = 0; c < N; ++c) s[c] = a.cap_log2 * tanh_wide(s[c] * a.cap_in);
               } else {
 #pragma unroll
-                for (int c = 0; c < HALF; c += 2) {
+                for (int c = 0; c < N; c += 2) {
                   const uint64_t v = ptx::f32x2(s[c], s[c + 1]);
                   ptx::f32x2_split(mul_f32x2(v, cap_poly(v, cap)), s[c], s[c + 1]);
                 }
@@ -653,20 +735,20 @@ __global__ void __launch_bounds__(512, 1)
               const float ff = fminf(f2 * a.scale_log2, 1e37f);
               const uint64_t f22 = ptx::f32x2(ff, ff);
 #pragma unroll
-              for (int c = 0; c < HALF; c += 2)
+              for (int c = 0; c < N; c += 2)
                 ptx::f32x2_split(mul_f32x2(ptx::f32x2(s[c], s[c + 1]), f22), s[c], s[c + 1]);
             }
             if (a.slopes) {
-              // a thread's 64 keys against its own row: one side or around it
-              const int c0 = t * C::BK + half * HALF;
-              const bool around = __any_sync(0xffffffffu, at > c0 && at < c0 + HALF - 1);
+              // a thread's keys against its own row: one side or around it
+              const int c0 = t * C::BK + key0;
+              const bool around = __any_sync(0xffffffffu, at > c0 && at < c0 + N - 1);
               if (around) add_bias(s, slope2, at, c0, 0);
               else add_bias(s, slope2, at, c0, at <= c0 ? 1 : -1);
             }
           }
-          if (valid < HALF) {
+          if (valid < N) {
 #pragma unroll
-            for (int c = 0; c < HALF; ++c)
+            for (int c = 0; c < N; ++c)
               if (c >= valid) s[c] = ninf;
           }
           float mx = row_max(s) * f;
@@ -699,9 +781,9 @@ __global__ void __launch_bounds__(512, 1)
           const float neg = (m == ninf ? 0.f : -m) + kPShift;
           const uint64_t f2x = ptx::f32x2(f, f), neg2 = ptx::f32x2(neg, neg);
           uint64_t acc0 = ptx::f32x2(0.f, 0.f), acc1 = acc0;
-          uint32_t pk[32];
+          uint32_t pk[N / 2];
 #pragma unroll
-          for (int e = 0; e < HALF / 2; ++e) {
+          for (int e = 0; e < N / 2; ++e) {
             float x0, x1;
             ptx::f32x2_split(ptx::fma_f32x2(ptx::f32x2(s[2 * e], s[2 * e + 1]), f2x, neg2), x0, x1);
             const float p0 = ptx::ex2(x0), p1 = ptx::ex2(x1);
@@ -709,7 +791,15 @@ __global__ void __launch_bounds__(512, 1)
             else acc0 = ptx::add_f32x2(acc0, ptx::f32x2(p0, p1));
             pk[e] = ptx::pack_f16x2(p0, p1);
           }
-          ptx::tmem_st16x2_32<HALF / 2>(lane_base + (b ? C::TM_S1 : C::TM_S0), pk);
+          const uint32_t p_taddr = lane_base + (b ? C::TM_S1 : C::TM_S0);
+          ptx::tmem_st16x2<N / 2>(p_taddr + copy * (COLS / 2), pk);
+          if constexpr (K > 1) {  // my lanes' P of the other copies' keys
+            uint32_t zero[N / 2];
+#pragma unroll
+            for (int e = 0; e < N / 2; ++e) zero[e] = 0u;
+#pragma unroll
+            for (int o = 1; o < K; ++o) ptx::tmem_st16x2<N / 2>(p_taddr + ((copy + o) % K) * (COLS / 2), zero);
+          }
           float a0, a1, b0, b1;
           ptx::f32x2_split(acc0, a0, a1);
           ptx::f32x2_split(acc1, b0, b1);
@@ -734,42 +824,107 @@ __global__ void __launch_bounds__(512, 1)
         break;
       }
       ptx::tc_fence_after();
-      if (warp_on) {
-        const float lt = l + __shfl_xor_sync(0xffffffffu, l, 16);
-        const bool empty = lt == 0.f;
-        const float f = (empty ? 0.f : 1.0f / lt) * pow2i(vref);
-        const float lse2 = empty ? ninf : m - kPShift + ptx::lg2(lt);
-        const bool whole = part.cnt == part.nt;
-        const long grow = (static_cast<long>(part.n) * a.Hkv + part.hk) * a.R + part.rt * 128 + r;
-        const long prow = static_cast<long>(2 * blockIdx.x + (part.t0 == 0 ? 1 : 0)) * a.part_rows + r;
-        uint4* o_dst = reinterpret_cast<uint4*>(a.o + grow * D) + half * (D / 16);
-        float4* p_dst = reinterpret_cast<float4*>(a.o_part + prow * D) + half * (D / 8);
+      const float lt = l + __shfl_xor_sync(0xffffffffu, l, 16);
+      const bool whole = part.cnt == part.nt;
+      const long grow0 = (static_cast<long>(part.n) * a.Hkv + part.hk) * a.R + part.rt * 128;
+      const long prow0 = static_cast<long>(2 * blockIdx.x + (part.t0 == 0 ? 1 : 0)) * a.part_rows;
+      // sums of my row over all copies
+      float M = m, L = lt;
+      if constexpr (K > 1) {
+        float2* ml = reinterpret_cast<float2*>(smem + C::OFF_J + C::J_BYTES);  // [copy][row]
+        constexpr int RB = 8 / K;  // row blocks
+        if (half == 0) ml[(copy * RB + rb) * 16 + (lane & 15)] = make_float2(m, lt);
+        if (!join()) {
+          ok = false;
+          break;
+        }
+        M = ninf;
+        L = 0.f;
+        if (warp_on) {
 #pragma unroll
-        for (int c = 0; c < D / 64; ++c) {
+          for (int o = 0; o < K; ++o) M = fmaxf(M, ml[(o * RB + rb) * 16 + (lane & 15)].x);
+#pragma unroll
+          for (int o = 0; o < K; ++o) {
+            const float2 x = ml[(o * RB + rb) * 16 + (lane & 15)];
+            L += x.y == 0.f ? 0.f : x.y * ptx::ex2(x.x - M);
+          }
+        }
+      }
+      const bool empty = L == 0.f;
+      // a copy that saw no key left m at -inf and its O at zero
+      const float share = K == 1 || m == M ? 1.f : (m == ninf ? 0.f : ptx::ex2(m - M));
+      const float f = (empty ? 0.f : share / L) * pow2i(vref);
+      if (row_valid && half == 0 && copy == 0) {
+        const float lse2 = empty ? ninf : M - kPShift + ptx::lg2(L);
+        if (whole) a.lse[grow0 + r] = lse2 * 0.69314718055994530942f;
+        else a.l_part[prow0 + r] = lse2;
+      }
+#pragma unroll
+      for (int c = 0; c < D / 64; ++c) {
+        float v[32];
+        if (warp_on) {
           uint32_t raw[32];
           ptx::tmem_ld16x2_32<D / 2>(lane_base + C::TM_O + c * 32, raw);
           ptx::tmem_wait_ld();
           ptx::reg_fence32(raw);
-          float v[32];
 #pragma unroll
-          for (int e = 0; e < 32; ++e) v[e] = empty ? 0.f : __uint_as_float(raw[e]) * f;
+          for (int e = 0; e < 32; ++e) v[e] = f == 0.f ? 0.f : __uint_as_float(raw[e]) * f;
+        }
+        if constexpr (K == 1) {
           if (row_valid) {
+            uint4* o_dst = reinterpret_cast<uint4*>(a.o + (grow0 + r) * D) + half * (D / 16) + c * 4;
+            float4* p_dst = reinterpret_cast<float4*>(a.o_part + (prow0 + r) * D) + half * (D / 8) + c * 8;
             if (whole) {
 #pragma unroll
               for (int u = 0; u < 4; ++u)
-                o_dst[c * 4 + u] = make_uint4(ptx::pack_bf16x2(v[8 * u], v[8 * u + 1]), ptx::pack_bf16x2(v[8 * u + 2], v[8 * u + 3]),
-                                              ptx::pack_bf16x2(v[8 * u + 4], v[8 * u + 5]), ptx::pack_bf16x2(v[8 * u + 6], v[8 * u + 7]));
+                o_dst[u] = make_uint4(ptx::pack_bf16x2(v[8 * u], v[8 * u + 1]), ptx::pack_bf16x2(v[8 * u + 2], v[8 * u + 3]),
+                                      ptx::pack_bf16x2(v[8 * u + 4], v[8 * u + 5]), ptx::pack_bf16x2(v[8 * u + 6], v[8 * u + 7]));
             } else {
 #pragma unroll
-              for (int u = 0; u < 8; ++u) p_dst[c * 8 + u] = make_float4(v[4 * u], v[4 * u + 1], v[4 * u + 2], v[4 * u + 3]);
+              for (int u = 0; u < 8; ++u) p_dst[u] = make_float4(v[4 * u], v[4 * u + 1], v[4 * u + 2], v[4 * u + 3]);
             }
           }
-        }
-        if (row_valid && half == 0) {
-          if (whole) a.lse[grow] = lse2 * 0.69314718055994530942f;
-          else a.l_part[prow] = lse2;
+        } else {
+          // [copy][row][16 float4], the float4 of a row permuted by the row
+          constexpr int RB = 8 / K;
+          float4* jb = reinterpret_cast<float4*>(smem + C::OFF_J);
+          if (c > 0 && !join()) {  // the previous columns have been read
+            ok = false;
+            break;
+          }
+          if (warp_on) {
+            float4* dst = jb + ((copy * RB + rb) * 16 + (lane & 15)) * 16;
+#pragma unroll
+            for (int u = 0; u < 8; ++u)
+              dst[(half * 8 + u) ^ (lane & 15)] = make_float4(v[4 * u], v[4 * u + 1], v[4 * u + 2], v[4 * u + 3]);
+          }
+          if (!join()) {
+            ok = false;
+            break;
+          }
+          const int tid = threadIdx.x;  // 0..255
+          for (int x = tid; x < rows * 16; x += 256) {
+            const int row = x >> 4, u = x & 15;
+            float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+            for (int o = 0; o < K; ++o) {
+              const float4 y = jb[(o * RB * 16 + row) * 16 + (u ^ (row & 15))];
+              sum.x += y.x;
+              sum.y += y.y;
+              sum.z += y.z;
+              sum.w += y.w;
+            }
+            // element: half u/8 of the row, 32 columns of this pass
+            const int e = (u >> 3) * (D / 2) + c * 32 + (u & 7) * 4;
+            if (whole)
+              *reinterpret_cast<uint2*>(a.o + (grow0 + row) * D + e) =
+                  make_uint2(ptx::pack_bf16x2(sum.x, sum.y), ptx::pack_bf16x2(sum.z, sum.w));
+            else
+              *reinterpret_cast<float4*>(a.o_part + (prow0 + row) * D + e) = sum;
+          }
         }
       }
+      if (!ok) break;
       // the next part's first PV overwrites O only after this warp's next PFULL
       // arrival, which follows the loads above
     }
@@ -785,22 +940,32 @@ __global__ void __launch_bounds__(512, 1)
 
 // Joins the partial results of items cut by the ends of runs:
 //   O = sum_i 2^(l_i - L) O_i,  L = log2 sum_i 2^(l_i)
-// in the order of the runs, and writes the rows of empty sequences. One CTA per
-// item (blockIdx.y: sequence, blockIdx.x: its kv head and row tile); a warp
-// takes whole rows. `runs`: the CTAs of the attention kernel.
+// in the order of the runs, and writes the rows of empty sequences.
+// blockIdx: item of the sequence (kv head and row tile), sequence, group of
+// kMergeRows rows. Thread c looks whether run c holds part of the item; a warp
+// then takes whole rows. `runs`: the CTAs of the attention kernel. Launched as
+// its programmatic dependent: only the part after grid_dep_wait reads its
+// results.
+constexpr int kMergeRows = 10;
 template <int D>
-__global__ void __launch_bounds__(128) cache_merge_kernel(const __grid_constant__ CacheArgs a, int runs) {
+__global__ void __launch_bounds__(kCacheMaxCtas) cache_merge_kernel(const __grid_constant__ CacheArgs a, int runs) {
   constexpr int V = D / 32;  // elements of a lane
-  ptx::grid_dep_wait();
+  constexpr int WARPS = kCacheMaxCtas / 32;
+  __shared__ int s_slot[kCacheMaxCtas];     // the item's slots in the order of the runs
+  __shared__ int s_count[WARPS];
+  __shared__ float s_w[WARPS][kCacheMaxCtas];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const float ninf = -__int_as_float(0x7f800000);
   const int n = blockIdx.y, item = blockIdx.x;
   const int hk = item / a.RT, rt = item - hk * a.RT;
-  const int rows = min(128, a.R - rt * 128);
+  const int r0 = blockIdx.z * kMergeRows;
+  const int r1 = min(min(128, a.R - rt * 128), r0 + kMergeRows);
+  if (r0 >= r1) return;
   const long grow0 = (static_cast<long>(n) * a.Hkv + hk) * a.R + rt * 128;
   const int nt = cache_tiles(cache_len(a, n));
   if (nt == 0) {
-    for (int r = warp; r < rows; r += 4) {
+    ptx::grid_dep_wait();  // O and LSE may still be read by what ran before the attention kernel
+    for (int r = r0 + warp; r < r1; r += WARPS) {
       for (int e = lane; e < D; e += 32) a.o[(grow0 + r) * D + e] = 0;
       if (lane == 0) a.lse[grow0 + r] = ninf;
     }
@@ -808,34 +973,49 @@ __global__ void __launch_bounds__(128) cache_merge_kernel(const __grid_constant_
   }
   long before;
   const long T = cache_total(a, lane, n, &before);
-  const long x0 = before + static_cast<long>(item) * nt, x1 = x0 + nt - 1;  // the item's tiles
-  // the runs that hold its first and last tile
-  int c0 = static_cast<int>(min(static_cast<long>(runs) - 1, x0 / max(1l, T / runs + 1)));
-  while (run_begin(T, c0 + 1, runs) <= x0) ++c0;
-  int c1 = c0;
-  while (run_begin(T, c1 + 1, runs) <= x1) ++c1;
-  if (c0 == c1) return;  // whole in one run: written there
-  for (int r = warp; r < rows; r += 4) {
-    float L = ninf;
-    for (int c = c0 + lane; c <= c1; c += 32)
-      if (run_begin(T, c, runs) < run_begin(T, c + 1, runs))
-        L = fmaxf(L, a.l_part[static_cast<long>(2 * c + (c == c0 ? 1 : 0)) * a.part_rows + r]);
+  const long x0 = before + static_cast<long>(item) * nt, x1 = x0 + nt;  // the item's tiles
+  const int c = threadIdx.x;
+  const long b0 = run_begin(T, c, runs), b1 = c < runs ? run_begin(T, c + 1, runs) : b0;
+  const bool holds = b0 < b1 && b0 < x1 && b1 > x0;
+  const uint32_t vote = __ballot_sync(0xffffffffu, holds);
+  if (lane == 0) s_count[warp] = __popc(vote);
+  __syncthreads();
+  int at = 0, count = 0;
+#pragma unroll
+  for (int w = 0; w < WARPS; ++w) {
+    at += w < warp ? s_count[w] : 0;
+    count += s_count[w];
+  }
+  if (count == 1) return;  // whole in one run: written there
+  if (holds) s_slot[at + __popc(vote & ((1u << lane) - 1u))] = 2 * c + (b0 <= x0 ? 1 : 0);
+  __syncthreads();
+  ptx::grid_dep_wait();
+  for (int r = r0 + warp; r < r1; r += WARPS) {
+    float L = ninf, l[WARPS];
+#pragma unroll
+    for (int u = 0; u < WARPS; ++u) {
+      const int i = u * 32 + lane;
+      l[u] = i < count ? a.l_part[static_cast<long>(s_slot[i]) * a.part_rows + r] : ninf;
+      L = fmaxf(L, l[u]);
+    }
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1) L = fmaxf(L, __shfl_xor_sync(0xffffffffu, L, off));
     const float base = L == ninf ? 0.f : L;
+#pragma unroll
+    for (int u = 0; u < WARPS; ++u) s_w[warp][u * 32 + lane] = ptx::ex2(l[u] - base);
+    __syncwarp();
     float sum = 0.f, acc[V];
 #pragma unroll
     for (int e = 0; e < V; ++e) acc[e] = 0.f;
-#pragma unroll 4
-    for (int c = c0; c <= c1; ++c) {
-      if (run_begin(T, c, runs) == run_begin(T, c + 1, runs)) continue;  // an empty run
-      const long prow = static_cast<long>(2 * c + (c == c0 ? 1 : 0)) * a.part_rows + r;
-      const float w = ptx::ex2(a.l_part[prow] - base);
+#pragma unroll 8
+    for (int i = 0; i < count; ++i) {
+      const float w = s_w[warp][i];
+      const float* src = a.o_part + (static_cast<long>(s_slot[i]) * a.part_rows + r) * D + lane * V;
       sum += w;
-      const float* src = a.o_part + prow * D + lane * V;
 #pragma unroll
       for (int e = 0; e < V; ++e) acc[e] += w * src[e];
     }
+    __syncwarp();
     const float inv = sum == 0.f ? 0.f : 1.0f / sum;
     uint32_t* dst = reinterpret_cast<uint32_t*>(a.o + (grow0 + r) * D) + lane * (V / 2);
 #pragma unroll

@@ -136,7 +136,7 @@ int make_map_cache(CUtensorMap* m, const uint8_t* ptr, long H, int C, int d, CUt
   return SPARSED_OK;
 }
 
-template <int D, bool MOD>
+template <int D, bool MOD, int K>
 int launch_cache_attn(const uint8_t* k8, const uint8_t* v8, const CacheArgs& a, cudaStream_t st) {
   using C = CacheCfg<D>;
   const unsigned items = static_cast<unsigned>(a.Hkv) * static_cast<unsigned>(a.RT);
@@ -147,7 +147,7 @@ int launch_cache_attn(const uint8_t* k8, const uint8_t* v8, const CacheArgs& a, 
   const long most = static_cast<long>(a.N) * items * cdiv(a.C, kCacheTile);
   const int runs = static_cast<int>(most < sms ? most : sms);
   if (runs > 0) {
-    auto kern = cache_attn_kernel<D, MOD>;
+    auto kern = cache_attn_kernel<D, MOD, K>;
     // the register split must be funded by the launch (as launch_attn_t)
     static int regs = -1;
     if (regs < 0) {
@@ -165,8 +165,9 @@ int launch_cache_attn(const uint8_t* k8, const uint8_t* v8, const CacheArgs& a, 
     kern<<<runs, C::THREADS, C::SMEM_BYTES, st>>>(tk, tv, a);
     SP_CUDA(cudaGetLastError());
   }
-  return launch_k(cache_merge_kernel<D>, dim3(items, static_cast<unsigned>(a.N)), dim3(128), 0, st, runs > 0, a,
-                  runs > 0 ? runs : 1);
+  const unsigned row_groups = static_cast<unsigned>(cdiv(a.R < 128 ? a.R : 128, kMergeRows));
+  return launch_k(cache_merge_kernel<D>, dim3(items, static_cast<unsigned>(a.N), row_groups), dim3(kCacheMaxCtas), 0,
+                  st, runs > 0, a, runs > 0 ? runs : 1);
 }
 
 }  // namespace
@@ -333,8 +334,24 @@ int sparsed_cache_attn(const uint16_t* Q, size_t q_stride_n, size_t q_stride_h, 
   if (items >= (1l << 31)) return SPARSED_ERR_UNSUPPORTED;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   const bool mod = a.capped || a.slopes;
-  if (d == 64) return mod ? launch_cache_attn<64, true>(k8, v8, a, st) : launch_cache_attn<64, false>(k8, v8, a, st);
-  return mod ? launch_cache_attn<128, true>(k8, v8, a, st) : launch_cache_attn<128, false>(k8, v8, a, st);
+  // as many copies of the rows as the accumulators' 128 lanes hold
+  const int copies = R <= 32 ? 4 : (R <= 64 ? 2 : 1);
+#define SP_CACHE(D_, MOD_, K_) \
+  if (d == D_ && mod == MOD_ && copies == K_) return launch_cache_attn<D_, MOD_, K_>(k8, v8, a, st);
+  SP_CACHE(64, false, 1)
+  SP_CACHE(64, false, 2)
+  SP_CACHE(64, false, 4)
+  SP_CACHE(64, true, 1)
+  SP_CACHE(64, true, 2)
+  SP_CACHE(64, true, 4)
+  SP_CACHE(128, false, 1)
+  SP_CACHE(128, false, 2)
+  SP_CACHE(128, false, 4)
+  SP_CACHE(128, true, 1)
+  SP_CACHE(128, true, 2)
+  SP_CACHE(128, true, 4)
+#undef SP_CACHE
+  return SPARSED_ERR_UNSUPPORTED;
 }
 
 int sparsed_document_ranges(const int32_t* starts, const int32_t* prefix, int n_docs, int L, int32_t* ranges,
