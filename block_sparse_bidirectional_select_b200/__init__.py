@@ -48,6 +48,7 @@ lse [H, L] fp32 natural log; kv_idx [H, nqb, kv_stride] int32 and kv_count
 from __future__ import annotations
 
 import ctypes
+import functools
 import math
 from dataclasses import dataclass
 
@@ -687,6 +688,12 @@ def run_steps_sharded(q, k, v, T, warmup_frac=0.2, keep=0.1, budget="entropy", r
 CACHE_BLOCK = 64  # tokens of a cache that share a scale
 
 
+# The raw handle of a device's current stream, without the Stream object that
+# torch.cuda.current_stream() makes (a microsecond a call).
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
 def _device_of(first, **tensors):
     """The CUDA device all given tensors (None left out) are on."""
     dev = first.device
@@ -698,63 +705,69 @@ def _device_of(first, **tensors):
     return dev
 
 
-def _check_strided(name, t, dims):
-    """A bf16 tensor of `dims` dimensions whose last one is contiguous."""
-    if not isinstance(t, torch.Tensor) or t.dtype != torch.bfloat16:
+def _strided(name, t, dims):
+    """Shape and leading strides of a bf16 tensor of `dims` dimensions whose
+    last one is contiguous. A dimension of size 1, whose stride says nothing,
+    gets the row's length."""
+    if not isinstance(t, torch.Tensor) or t.dtype is not torch.bfloat16:
         raise TypeError(f"{name} must be a bfloat16 torch.Tensor")
-    if t.dim() != dims:
-        raise ValueError(f"{name} must have {dims} dimensions, got {tuple(t.shape)}")
-    if t.shape[-1] != 1 and t.stride(-1) != 1:
+    shape, stride = t.shape, t.stride()
+    if len(shape) != dims:
+        raise ValueError(f"{name} must have {dims} dimensions, got {tuple(shape)}")
+    d = shape[-1]
+    if stride[-1] != 1 and d != 1:
         raise ValueError(f"{name}: the last dimension must be contiguous")
-
-
-def _strides(t):
-    """Strides of all dimensions but the last; d for one of size 1, whose stride says nothing."""
-    d = t.shape[-1]
-    return [st if n > 1 else d for st, n in zip(t.stride()[:-1], t.shape)]
+    return shape, [st if n > 1 else d for st, n in zip(stride[:-1], shape)]
 
 
 def _check_flat(name, t, dtype, shape):
-    if t.dtype != dtype or tuple(t.shape) != tuple(shape) or not t.is_contiguous():
+    if t.dtype is not dtype or t.shape != shape or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)}, "
                          f"got {t.dtype} {tuple(t.shape)}")
 
 
-class _Launch:
-    """The device and stream of one call: makes `dev` current, and yields the
-    stream handle. Tensors handed to `keep` (allocated on the current stream)
-    stay reserved until the work on a stream given by the caller is done."""
-
-    def __init__(self, dev, stream):
-        self.index = dev.index if dev.index is not None else torch.cuda.current_device()
-        self.stream = stream
-        self.guard = None
-
-    def __enter__(self):
-        if self.index != torch.cuda.current_device():
-            self.guard = torch.cuda.device(self.index)
-            self.guard.__enter__()
-        self.handle = (torch.cuda.current_stream(self.index) if self.stream is None else self.stream).cuda_stream
-        return self
-
-    def __exit__(self, *exc):
-        if self.guard is not None:
-            self.guard.__exit__(*exc)
-
-    def keep(self, *tensors):
-        if self.stream is not None:
-            for t in tensors:
-                if t is not None:
-                    t.record_stream(self.stream)
+def _launch(name, dev, stream, keep, args):
+    """Calls the entry point with `dev` current, on its current stream or on
+    `stream`. For a stream given by the caller, the tensors in `keep` (which
+    may be freed before its work is done) are recorded on it."""
+    fn = getattr(_lib.load(), name)
+    index = dev.index
+    if stream is None:
+        handle = _raw_stream(index)
+    else:
+        handle = stream.cuda_stream
+        for t in keep:
+            if t is not None:
+                t.record_stream(stream)
+    if index == torch.cuda.current_device():
+        rc = fn(*args, handle)
+    else:
+        with torch.cuda.device(index):
+            rc = fn(*args, handle)
+    if rc != _lib.OK:
+        raise SparsedError(rc, name)
 
 
-def _out_like(name, out, shape, dtype, dev):
+def _out_like(name, out, like, shape, dtype):
     if out is None:
-        return torch.empty(shape, dtype=dtype, device=dev)
+        return like.new_empty(shape, dtype=dtype)
     _check_flat(name, out, dtype, shape)
-    if out.device != dev:
-        raise ValueError(f"{name} must be on {dev}")
+    if out.device != like.device:
+        raise ValueError(f"{name} must be on {like.device}")
     return out
+
+
+def _data(t):
+    return None if t is None else t.data_ptr()
+
+
+@functools.lru_cache(maxsize=64)
+def _sections(sections):
+    """A ctypes array of the sections (kept, so that its address stays valid)."""
+    return (ctypes.c_int * max(len(sections), 1))(*sections)
+
+
+_default_scale = functools.lru_cache(maxsize=16)(default_scale)
 
 
 def rope_axes(x, positions, sections, theta=10000.0, interleaved=False, shared_ladder=False, inverse=False,
@@ -767,26 +780,24 @@ def rope_axes(x, positions, sections, theta=10000.0, interleaved=False, shared_l
     i-th pair, or theta^-(j / J) with shared_ladder. ``inverse`` turns the
     other way (the gradient's rotation). Returns y [H, L, d]: contiguous, or
     ``out`` (any strides; may be x)."""
-    _check_strided("x", x, 3)
-    H, L, d = x.shape
-    sections = tuple(int(n) for n in sections)
-    if not isinstance(positions, torch.Tensor) or positions.dtype != torch.int32 or not positions.is_contiguous() \
-            or tuple(positions.shape) != (len(sections), L):
-        raise ValueError(f"positions must be a contiguous int32 tensor [{len(sections)}, {L}]")
-    dev = _device_of(x, positions=positions, out=out)
+    shape, xs = _strided("x", x, 3)
+    H, L, d = shape
+    pairs = _sections(tuple(sections))
+    axes = len(sections)
+    if not isinstance(positions, torch.Tensor):
+        raise TypeError("positions must be a torch.Tensor")
+    _check_flat("positions", positions, torch.int32, (axes, L))
     if out is None:
-        out = torch.empty((H, L, d), dtype=torch.bfloat16, device=dev)
+        dev = _device_of(x, positions=positions)
+        out, ys = x.new_empty(shape), (L * d, d)
     else:
-        _check_strided("out", out, 3)
-        if out.shape != x.shape:
-            raise ValueError(f"out must be shaped {tuple(x.shape)}, got {tuple(out.shape)}")
-    pairs = (ctypes.c_int * max(len(sections), 1))(*sections)
-    with _Launch(dev, stream) as at:
-        at.keep(x, positions, out)
-        rc = _lib.load().sparsed_rope_axes(
-            x.data_ptr(), *_strides(x), positions.data_ptr(), len(sections), ctypes.addressof(pairs), H, L, d, theta,
-            int(interleaved), int(shared_ladder), int(inverse), out.data_ptr(), *_strides(out), at.handle)
-    check(rc, "sparsed_rope_axes")
+        dev = _device_of(x, positions=positions, out=out)
+        out_shape, ys = _strided("out", out, 3)
+        if out_shape != shape:
+            raise ValueError(f"out must be shaped {tuple(shape)}, got {tuple(out_shape)}")
+    _launch("sparsed_rope_axes", dev, stream, (x, positions, out),
+            (x.data_ptr(), xs[0], xs[1], positions.data_ptr(), axes, ctypes.addressof(pairs), H, L, d, theta,
+             int(interleaved), int(shared_ladder), int(inverse), out.data_ptr(), ys[0], ys[1]))
     return out
 
 
@@ -810,15 +821,17 @@ def cache_alloc(N: int, H: int, C: int, d: int, device="cuda") -> Cache8:
 
 
 def _check_cache(cache):
-    shape = cache.k8.shape
+    k8, v8, ks, vs = cache.k8, cache.v8, cache.k_scale, cache.v_scale
+    shape = k8.shape
     if len(shape) != 4 or shape[2] % CACHE_BLOCK != 0:
         raise ValueError(f"the cache must be [N, Hkv, C, d] with C a multiple of {CACHE_BLOCK}, got {tuple(shape)}")
     N, H, C, d = shape
-    for name, t in (("k8", cache.k8), ("v8", cache.v8)):
-        _check_flat(name, t, torch.float8_e4m3fn, shape)
-    for name, t in (("k_scale", cache.k_scale), ("v_scale", cache.v_scale)):
-        _check_flat(name, t, torch.float32, (N, H, C // CACHE_BLOCK))
-    return N, H, C, d
+    blocks = (N, H, C // CACHE_BLOCK)
+    _check_flat("k8", k8, torch.float8_e4m3fn, shape)
+    _check_flat("v8", v8, torch.float8_e4m3fn, shape)
+    _check_flat("k_scale", ks, torch.float32, blocks)
+    _check_flat("v_scale", vs, torch.float32, blocks)
+    return N, H, C, d, _device_of(k8, v8=v8, k_scale=ks, v_scale=vs)
 
 
 def cache_append(cache: Cache8, k, v, start, count=None, stream=None) -> Cache8:
@@ -826,27 +839,24 @@ def cache_append(cache: Cache8, k, v, start, count=None, stream=None) -> Cache8:
     contiguous) into the cache: the first count[n] tokens (default: all B) of
     sequence n at positions start[n] on; start, count [N] int32. Tokens of the
     cache at or past start + count are no longer valid."""
-    _check_strided("k", k, 4)
-    _check_strided("v", v, 4)
-    N, H, C, d = _check_cache(cache)
-    B = k.shape[2]
-    if k.shape != v.shape or tuple(k.shape) != (N, H, B, d):
-        raise ValueError(f"k and v must be [{N}, {H}, B, {d}], got {tuple(k.shape)} and {tuple(v.shape)}")
+    shape, ks = _strided("k", k, 4)
+    v_shape, vs = _strided("v", v, 4)
+    N, H, C, d, dev = _check_cache(cache)
+    B = shape[2]
+    if shape != v_shape or shape != (N, H, B, d):
+        raise ValueError(f"k and v must be [{N}, {H}, B, {d}], got {tuple(shape)} and {tuple(v_shape)}")
     _check_flat("start", start, torch.int32, (N,))
     if count is not None:
         _check_flat("count", count, torch.int32, (N,))
-    dev = _device_of(cache.k8, v8=cache.v8, k_scale=cache.k_scale, v_scale=cache.v_scale, k=k, v=v, start=start,
-                     count=count)
-    with _Launch(dev, stream) as at:
-        at.keep(k, v, start, count)
-        rc = _lib.load().sparsed_cache_append(
-            k.data_ptr(), *_strides(k), v.data_ptr(), *_strides(v), N, H, B, C, d, start.data_ptr(),
-            None if count is None else count.data_ptr(), cache.k8.data_ptr(), cache.v8.data_ptr(),
-            cache.k_scale.data_ptr(), cache.v_scale.data_ptr(), at.handle)
-    check(rc, "sparsed_cache_append")
+    _device_of(cache.k8, k=k, v=v, start=start, count=count)
+    _launch("sparsed_cache_append", dev, stream,
+            (k, v, start, count, cache.k8, cache.v8, cache.k_scale, cache.v_scale),
+            (k.data_ptr(), *ks, v.data_ptr(), *vs, N, H, B, C, d, start.data_ptr(), _data(count),
+             cache.k8.data_ptr(), cache.v8.data_ptr(), cache.k_scale.data_ptr(), cache.v_scale.data_ptr()))
     return cache
 
 
+@functools.lru_cache(maxsize=256)
 def cache_attn_workspace_bytes(N: int, Hq: int, Hkv: int, B: int, d: int) -> int:
     n = ctypes.c_size_t()
     check(_lib.load().sparsed_cache_attn_workspace_bytes(N, Hq, Hkv, B, d, ctypes.byref(n)),
@@ -863,31 +873,27 @@ def cache_attn(q, cache: Cache8, lengths, scale=None, softcap=0.0, slopes=None, 
     slopes[h] * |position - key|, with the first query token of sequence n at
     q_start[n] (default lengths[n] - B: the block is the cache's last B
     tokens). lengths, q_start: [N] int32 on the device."""
-    _check_strided("q", q, 4)
-    N, Hkv, C, d = _check_cache(cache)
-    Hq, B = q.shape[1], q.shape[2]
-    if q.shape[0] != N or q.shape[3] != d or Hkv == 0 or Hq % Hkv != 0:
-        raise ValueError(f"q {tuple(q.shape)} does not fit a cache of {N} sequences, {Hkv} heads, d={d}")
+    shape, qs = _strided("q", q, 4)
+    N, Hkv, C, d, dev = _check_cache(cache)
+    Hq, B = shape[1], shape[2]
+    if shape[0] != N or shape[3] != d or Hkv == 0 or Hq % Hkv != 0:
+        raise ValueError(f"q {tuple(shape)} does not fit a cache of {N} sequences, {Hkv} heads, d={d}")
     _check_flat("lengths", lengths, torch.int32, (N,))
     if q_start is not None:
         _check_flat("q_start", q_start, torch.int32, (N,))
     if slopes is not None:
         _check_flat("slopes", slopes, torch.float32, (Hq,))
-    dev = _device_of(q, k8=cache.k8, v8=cache.v8, k_scale=cache.k_scale, v_scale=cache.v_scale, lengths=lengths,
-                     q_start=q_start, slopes=slopes, workspace=workspace)
-    out = _out_like("out", out, (N, Hq, B, d), torch.bfloat16, dev)
-    lse = _out_like("lse", lse, (N, Hq, B), torch.float32, dev)
+    _device_of(cache.k8, q=q, lengths=lengths, q_start=q_start, slopes=slopes, workspace=workspace)
+    out = _out_like("out", out, q, shape, torch.bfloat16)
+    lse = _out_like("lse", lse, q, shape[:3], torch.float32)
     if workspace is None:
-        workspace = torch.empty(cache_attn_workspace_bytes(N, Hq, Hkv, B, d), dtype=torch.uint8, device=dev)
-    with _Launch(dev, stream) as at:
-        at.keep(q, cache.k8, cache.v8, cache.k_scale, cache.v_scale, lengths, q_start, slopes, out, lse, workspace)
-        rc = _lib.load().sparsed_cache_attn(
-            q.data_ptr(), *_strides(q), cache.k8.data_ptr(), cache.v8.data_ptr(),
-            cache.k_scale.data_ptr(), cache.v_scale.data_ptr(), N, Hq, Hkv, B, C, d, lengths.data_ptr(),
-            None if q_start is None else q_start.data_ptr(), default_scale(d) if scale is None else scale, softcap,
-            None if slopes is None else slopes.data_ptr(), out.data_ptr(), lse.data_ptr(), workspace.data_ptr(),
-            workspace.numel(), at.handle)
-    check(rc, "sparsed_cache_attn")
+        workspace = q.new_empty(cache_attn_workspace_bytes(N, Hq, Hkv, B, d), dtype=torch.uint8)
+    _launch("sparsed_cache_attn", dev, stream,
+            (q, cache.k8, cache.v8, cache.k_scale, cache.v_scale, lengths, q_start, slopes, out, lse, workspace),
+            (q.data_ptr(), *qs, cache.k8.data_ptr(), cache.v8.data_ptr(), cache.k_scale.data_ptr(),
+             cache.v_scale.data_ptr(), N, Hq, Hkv, B, C, d, lengths.data_ptr(), _data(q_start),
+             _default_scale(d) if scale is None else scale, softcap, _data(slopes), out.data_ptr(), lse.data_ptr(),
+             workspace.data_ptr(), workspace.numel()))
     return out, lse
 
 
@@ -904,15 +910,13 @@ def document_ranges(starts, L: int, prefix=None, stream=None):
     if prefix is not None:
         _check_flat("prefix", prefix, torch.int32, (n,))
     dev = _device_of(starts, prefix=prefix)
-    ranges = torch.empty((L, 2), dtype=torch.int32, device=dev)
-    with _Launch(dev, stream) as at:
-        at.keep(starts, prefix, ranges)
-        rc = _lib.load().sparsed_document_ranges(starts.data_ptr(), None if prefix is None else prefix.data_ptr(), n,
-                                                 L, ranges.data_ptr(), at.handle)
-    check(rc, "sparsed_document_ranges")
+    ranges = starts.new_empty((L, 2))
+    _launch("sparsed_document_ranges", dev, stream, (starts, prefix, ranges),
+            (starts.data_ptr(), _data(prefix), n, L, ranges.data_ptr()))
     return ranges
 
 
+@functools.lru_cache(maxsize=256)
 def scored_attn_workspace_bytes(Hq: int, Lq: int) -> int:
     n = ctypes.c_size_t()
     check(_lib.load().sparsed_scored_attn_workspace_bytes(Hq, Lq, ctypes.byref(n)),
@@ -928,27 +932,24 @@ def scored_attn(q, k, v, scale=None, softcap=0.0, slopes=None, ranges=None, q_st
     softcap * tanh(x / softcap); ``slopes`` [Hq] fp32 subtracts
     slopes[h] * |q_start + r - c|; ``ranges`` [Lq, 2] int32 gives the keys
     [lo, hi) that every row sees (document_ranges; default: all)."""
-    for name, t in (("q", q), ("k", k), ("v", v)):
-        _check_strided(name, t, 3)
-    Hq, Lq, d = q.shape
-    Hkv, Lk = k.shape[0], k.shape[1]
-    if k.shape != v.shape or k.shape[2] != d or Hkv == 0 or Hq % Hkv != 0:
-        raise ValueError(f"q {tuple(q.shape)}, k {tuple(k.shape)} and v {tuple(v.shape)} do not fit")
+    shape, qs = _strided("q", q, 3)
+    k_shape, ks = _strided("k", k, 3)
+    v_shape, vs = _strided("v", v, 3)
+    Hq, Lq, d = shape
+    Hkv, Lk = k_shape[0], k_shape[1]
+    if k_shape != v_shape or k_shape[2] != d or Hkv == 0 or Hq % Hkv != 0:
+        raise ValueError(f"q {tuple(shape)}, k {tuple(k_shape)} and v {tuple(v_shape)} do not fit")
     if slopes is not None:
         _check_flat("slopes", slopes, torch.float32, (Hq,))
     if ranges is not None:
         _check_flat("ranges", ranges, torch.int32, (Lq, 2))
     dev = _device_of(q, k=k, v=v, slopes=slopes, ranges=ranges, workspace=workspace)
-    out = _out_like("out", out, (Hq, Lq, d), torch.bfloat16, dev)
-    lse = _out_like("lse", lse, (Hq, Lq), torch.float32, dev)
+    out = _out_like("out", out, q, shape, torch.bfloat16)
+    lse = _out_like("lse", lse, q, shape[:2], torch.float32)
     if workspace is None:
-        workspace = torch.empty(scored_attn_workspace_bytes(Hq, Lq), dtype=torch.uint8, device=dev)
-    with _Launch(dev, stream) as at:
-        at.keep(q, k, v, slopes, ranges, out, lse, workspace)
-        rc = _lib.load().sparsed_scored_attn(
-            q.data_ptr(), *_strides(q), k.data_ptr(), *_strides(k), v.data_ptr(), *_strides(v), Hq,
-            Hkv, Lq, Lk, d, default_scale(d) if scale is None else scale, softcap,
-            None if slopes is None else slopes.data_ptr(), q_start, None if ranges is None else ranges.data_ptr(),
-            out.data_ptr(), lse.data_ptr(), workspace.data_ptr(), workspace.numel(), at.handle)
-    check(rc, "sparsed_scored_attn")
+        workspace = q.new_empty(scored_attn_workspace_bytes(Hq, Lq), dtype=torch.uint8)
+    _launch("sparsed_scored_attn", dev, stream, (q, k, v, slopes, ranges, out, lse, workspace),
+            (q.data_ptr(), *qs, k.data_ptr(), *ks, v.data_ptr(), *vs, Hq, Hkv, Lq, Lk, d,
+             _default_scale(d) if scale is None else scale, softcap, _data(slopes), q_start, _data(ranges),
+             out.data_ptr(), lse.data_ptr(), workspace.data_ptr(), workspace.numel()))
     return out, lse

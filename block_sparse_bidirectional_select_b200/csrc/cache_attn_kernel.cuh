@@ -6,7 +6,9 @@
 //
 // Rows. A kv head's query rows (its query heads times B tokens) are cut into
 // row tiles of up to 128; an item is one row tile of one kv head of one
-// sequence. Its keys are walked in tiles of 128 (two scale blocks).
+// sequence. Its keys are walked in tiles, last first (with a distance bias the
+// keys near the queries then set the row maxima at once; ascending, O would be
+// rescaled at every tile).
 //
 // Work split. All key tiles of all items, in order, are dealt out as one run
 // of equal length per CTA, whatever the sequences' lengths, so every SM reads
@@ -28,25 +30,32 @@
 // the run's part of the item (a power of two: exact, or below 2^-24 of that
 // scale), so O accumulates in one unit.
 //
-// Few rows. A row tile of at most 64 (32) rows is held 2 (4) times in the 128
-// lanes of the accumulators, and copy i takes the keys i*128/K .. of every tile:
-// its P is zero elsewhere, so each copy is a softmax of its own over its keys.
-// The tensor cores do the same work as for 128 rows; the softmax warps, whose
-// time per tile is a row's length and not the number of rows, get a half (a
-// quarter) each and run on all four schedulers. The copies are joined through
-// shared memory when an item's part ends.
+// Many rows (Q == 0, more than 64 rows of a kv head): tiles of 128 keys. All
+// eight softmax warps work on every tile, each 16 lanes of the accumulators
+// with 64 keys to a thread; P is written over the first half of its S.
+//
+// Few rows (Q == 1, 2, 4: at most 64, 32, 16 rows): what bounds the pass is then
+// the chain load S - maximum - exponentials - store P of one tile, a fixed cost
+// of several hundred clocks that does not shrink with the rows. So the rows are
+// held 2 * Q times in the 128 lanes, each copy a softmax of its own over its
+// part of the keys: lanes 0-15 of every quarter take the even tiles (warps 0-3),
+// lanes 16-31 the odd ones (warps 4-7), so two tiles are in work at any time; and
+// Q quarters that hold the same rows take a Q-th of a tile's keys each. A copy's
+// P is zero for the keys of the others: P has columns of its own, which are
+// cleared once and written only by their owners. With 64 keys to a tile, S, P
+// and Q all fit twice, and S(g+2) starts when S(g) has been read. The copies
+// are joined through shared memory when an item's part ends.
 //
 // Warp roles (512 threads):
 //   warps 0-7   softmax: warp w covers the lanes 32*(w%4) + 16*(w/4) + 0..15, thread
-//               t lane t%16 and half t/16 of its copy's keys; they also bring each
-//               item's Q into TMEM as hi and lo
+//               t lane t%16 and half t/16 of its keys; they also bring each item's
+//               Q into TMEM as hi and lo
 //   warp 8      TMA producer: K and V tiles
 //   warp 9      TMEM owner; issues S
 //   warp 10     issues O += P V
 //   warp 11     idle
 //   warps 12-15 widen V tiles (e4m3 -> f16, rows past the length cleared)
-// TMEM: [S0 | S1 | O | Q0 | Q1], P over the first half of its S.
-// Barriers and orders otherwise as attn_list_kernel. Every wait is bounded.
+// Every wait is bounded.
 #pragma once
 
 #include "cache_kernels.cuh"
@@ -54,7 +63,6 @@
 
 namespace sparsed {
 
-constexpr int kCacheTile = 128;
 constexpr int kCacheMaxCtas = 160;
 constexpr float kPShift = 7.0f;  // P's top is 2^7 when its row maximum is fresh
 
@@ -67,6 +75,7 @@ struct CacheArgs {
   int N, Hkv, group, B, C;
   int R, RT;                       // rows of a kv head, row tiles
   int part_rows;                   // rows of a partial result's slot
+  int tile;                        // keys of a tile
   float scale_log2;                // above 0
   const float* slopes;             // or null
   float cap_c[5];                  // as ScoredArgs
@@ -79,52 +88,68 @@ struct CacheArgs {
   uint64_t timeout_ns;
 };
 
-template <int D>
+template <int D, int Q>
 struct CacheCfg {
-  static constexpr int BK = kCacheTile;
-  static constexpr int T8 = BK * D;           // bytes of an e4m3 tile
+  static constexpr bool FEW = Q > 0;
+  static constexpr int BK = FEW ? 64 : 128;      // keys of a tile
+  static constexpr int COLS = FEW ? BK / Q : BK; // keys of a tile for one copy of the rows
+  static constexpr int N = COLS / 2;             // ... for one thread
+  static constexpr int T8 = BK * D;              // bytes of an e4m3 tile
   static constexpr int T16 = 2 * T8;
-  static constexpr int KS = D == 128 ? 4 : 8;
-  static constexpr int VS = KS;
+  static constexpr int KS = D == 64 ? 8 : (FEW ? 6 : 4);  // ring stages of K and of V
+  static constexpr int ROWS = FEW ? 64 / Q : 128;        // rows of a row tile at most
   static constexpr int OFF_K = 0;
   static constexpr int OFF_V = OFF_K + KS * T8;
-  static constexpr int OFF_W = OFF_V + VS * T8;  // widened V, 2 buffers
-  static constexpr int OFF_J = OFF_W + 2 * T16;  // joining copies: 8 warps x 16 lanes x 64 fp32, then (m, l) of each lane
-  static constexpr int J_BYTES = 8 * 16 * 64 * 4;
-  static constexpr int OFF_BAR = OFF_J + J_BYTES + 8 * 16 * 8;
+  static constexpr int WS = FEW ? 4 : 2;         // buffers of widened V
+  static constexpr int OFF_W = OFF_V + KS * T8;
+  static constexpr int OFF_J = OFF_W + WS * T16;  // joining copies: 128 lanes x 64 fp32, then (m, l) of each lane
+  static constexpr int J_BYTES = FEW ? 128 * 64 * 4 : 0;
+  static constexpr int OFF_Q = OFF_J + J_BYTES + (FEW ? 128 * 8 : 0);  // a part's Q: hi, lo, exponents
+  static constexpr int OFF_BAR = OFF_Q + 2 * ROWS * D + ROWS * 4;
   static constexpr int B_KFULL = 0;
   static constexpr int B_KEMPTY = B_KFULL + KS;
   static constexpr int B_VFULL = B_KEMPTY + KS;
-  static constexpr int B_VEMPTY = B_VFULL + VS;  // 4 converter-warp arrivals
-  static constexpr int B_WFULL = B_VEMPTY + VS;  // [2] 4 converter-warp arrivals
-  static constexpr int B_SFULL = B_WFULL + 2;    // [2]
-  static constexpr int B_PFULL = B_SFULL + 2;    // [2] 8 softmax-warp arrivals
-  static constexpr int B_PVDONE = B_PFULL + 2;   // [2] also frees the widened V
+  static constexpr int B_VEMPTY = B_VFULL + KS;  // 4 converter-warp arrivals
+  static constexpr int B_WFULL = B_VEMPTY + KS;  // [WS] 4 converter-warp arrivals
+  static constexpr int B_WEMPTY = B_WFULL + WS;  // [WS]
+  static constexpr int B_SFULL = B_WEMPTY + WS;  // [2]
+  static constexpr int B_SREAD = B_SFULL + 2;    // [2] FEW: S read, its owners' 4 warp arrivals
+  static constexpr int B_PFULL = B_SREAD + 2;    // [2] its owners' warp arrivals
+  static constexpr int B_PVDONE = B_PFULL + 2;   // [2]
   static constexpr int B_DRAIN = B_PVDONE + 2;   // [2]
   static constexpr int B_QTFULL = B_DRAIN + 2;   // [2] 8 softmax-warp arrivals
   static constexpr int B_QTEMPTY = B_QTFULL + 2; // [2]
   static constexpr int B_JOIN = B_QTEMPTY + 2;   // 8 softmax-warp arrivals
   static constexpr int NUM_BARS = B_JOIN + 1;
+  static constexpr int OWNERS = FEW ? 4 : 8;     // softmax warps that work on a tile
   static constexpr int OFF_MISC = OFF_BAR + NUM_BARS * 8;  // tmem slot, abort flag, run
   static constexpr int SMEM_BYTES = OFF_MISC + 48 + 1024;
+  // TMEM columns: S0, S1, then P0, P1 (or P over the first half of S), O, Q0, Q1
   static constexpr int TM_S0 = 0;
   static constexpr int TM_S1 = BK;
-  static constexpr int TM_O = 2 * BK;
-  static constexpr int TM_Q0 = 2 * BK + D;  // hi: D/4 columns of four e4m3, lo: D/4
+  static constexpr int TM_P0 = FEW ? 2 * BK : TM_S0;
+  static constexpr int TM_P1 = FEW ? 2 * BK + BK / 2 : TM_S1;
+  static constexpr int TM_O = FEW ? 3 * BK : 2 * BK;
+  static constexpr int TM_Q0 = TM_O + D;    // hi: D/4 columns of four e4m3, lo: D/4
   static constexpr int TM_Q1 = TM_Q0 + D / 2;
   static constexpr int TM_ALLOC = 512;
   // f32 accumulators; e4m3 x e4m3 (kind::f8f6f4) and f16 x f16 (kind::f16) are both format 0
-  static constexpr uint32_t idesc(int N, int b_mn) {
-    return (1u << 4) | (static_cast<uint32_t>(b_mn) << 16) | (static_cast<uint32_t>(N >> 3) << 17) | (8u << 24);
+  static constexpr uint32_t idesc(int n, int b_mn) {
+    return (1u << 4) | (static_cast<uint32_t>(b_mn) << 16) | (static_cast<uint32_t>(n >> 3) << 17) | (8u << 24);
   }
   static constexpr uint32_t IDESC_S = idesc(BK, 0);
   static constexpr uint32_t IDESC_PV = idesc(D, 1);
   // K rows of D bytes: one swizzle span of 128 or 64 bytes, 8 rows a group
   static constexpr uint32_t HI_K = ((8u * D) >> 4) | (1u << 14) | ((D == 128 ? 2u : 4u) << 29);
   static constexpr int THREADS = 512;
-  static constexpr int REGS_SOFTMAX = 184, REGS_CONTROL = 56, REGS_WIDEN = 88;
+  // Few rows leave 8192 registers and some shared memory of an SM to the merge
+  // kernel, whose CTAs then wait in place while the last runs end.
+  static constexpr int REGS_LAUNCH = FEW ? 112 : 128;
+  static constexpr int REGS_SOFTMAX = FEW ? 152 : 184, REGS_CONTROL = 56, REGS_WIDEN = FEW ? 80 : 88;
+  static constexpr int REGS_TOTAL = 256 * REGS_SOFTMAX + 128 * REGS_CONTROL + 128 * REGS_WIDEN;
   static_assert(TM_Q1 + D / 2 <= 512, "TMEM budget");
-  static_assert(SMEM_BYTES <= 232448, "shared memory budget");
+  static_assert(SMEM_BYTES <= (FEW ? 225280 : 232448), "shared memory budget");
+  static_assert(REGS_TOTAL <= REGS_LAUNCH * THREADS, "register budget");
 };
 
 namespace ptx {
@@ -178,23 +203,45 @@ template <int SPLIT>
 __device__ __forceinline__ void tmem_st16x2(uint32_t taddr, const uint32_t (&r)[32]) {
   tmem_st16x2_32<SPLIT>(taddr, r);
 }
+template <int SPLIT>
+__device__ __forceinline__ void tmem_ld16x2(uint32_t taddr, uint32_t (&r)[8]) {
+  asm volatile("tcgen05.ld.sync.aligned.16x32bx2.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8], %9;"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+               : "r"(taddr), "n"(SPLIT)
+               : "memory");
+}
+template <int SPLIT>
+__device__ __forceinline__ void tmem_st16x2(uint32_t taddr, const uint32_t (&r)[4]) {
+  asm volatile("tcgen05.st.sync.aligned.16x32bx2.x4.b32 [%0], %5, {%1,%2,%3,%4};" ::"r"(taddr), "r"(r[0]), "r"(r[1]),
+               "r"(r[2]), "r"(r[3]), "n"(SPLIT)
+               : "memory");
+}
+__device__ __forceinline__ void reg_fence8(uint32_t (&r)[8]) {
+  asm volatile("" : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]));
+}
 // Keeps uses of r below a preceding tmem_wait_ld (as reg_fence32).
 __device__ __forceinline__ void reg_fence16(uint32_t (&r)[16]) {
   asm volatile("" : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
                "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]));
 }
-__device__ __forceinline__ void setmaxnreg_inc_184() { asm volatile("setmaxnreg.inc.sync.aligned.u32 184;" ::: "memory"); }
-__device__ __forceinline__ void setmaxnreg_dec_88() { asm volatile("setmaxnreg.dec.sync.aligned.u32 88;" ::: "memory"); }
+template <int R>
+__device__ __forceinline__ void setmaxnreg_inc() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(R) : "memory");
+}
+template <int R>
+__device__ __forceinline__ void setmaxnreg_dec() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(R) : "memory");
+}
 }  // namespace ptx
 
 __device__ __forceinline__ int cache_len(const CacheArgs& a, int n) { return min(max(a.lengths[n], 0), a.C); }
-__device__ __forceinline__ int cache_tiles(int len) { return (len + kCacheTile - 1) / kCacheTile; }
+__device__ __forceinline__ int cache_tiles(const CacheArgs& a, int len) { return (len + a.tile - 1) / a.tile; }
 
 // Total key tiles of the call, and those before sequence n_stop (one warp).
 __device__ __forceinline__ long cache_total(const CacheArgs& a, int lane, int n_stop, long* before) {
   long t = 0, b = 0;
   for (int n = lane; n < a.N; n += 32) {
-    const long x = static_cast<long>(cache_tiles(cache_len(a, n))) * a.Hkv * a.RT;
+    const long x = static_cast<long>(cache_tiles(a, cache_len(a, n))) * a.Hkv * a.RT;
     t += x;
     if (n < n_stop) b += x;
   }
@@ -221,30 +268,37 @@ struct CachePart {
   int t0, cnt;     // this part's tiles
 };
 struct CacheRun {
-  int n, len, nt;
-  long off, left;
+  int n, hk, rt, t;  // where the run stands: item, tile
+  int len, nt;       // of sequence n
+  int left;          // tiles to go
   __device__ __forceinline__ void load(const CacheArgs& a) {
     len = cache_len(a, n);
-    nt = cache_tiles(len);
+    nt = cache_tiles(a, len);
   }
-  __device__ __forceinline__ bool next(const CacheArgs& a, CachePart* p) {
+  __device__ __forceinline__ bool next(const CacheArgs& a, CachePart& p) {
     if (left <= 0) return false;
-    while (off >= static_cast<long>(nt) * a.Hkv * a.RT) {
-      off = 0;
-      ++n;
-      if (n >= a.N) return false;
-      load(a);
+    if (t >= nt) {  // the next item, past empty sequences
+      t = 0;
+      if (++rt >= a.RT) {
+        rt = 0;
+        if (++hk >= a.Hkv) {
+          hk = 0;
+          do {
+            if (++n >= a.N) return false;
+            load(a);
+          } while (nt == 0);
+        }
+      }
     }
-    const int item = static_cast<int>(off / nt);
-    p->n = n;
-    p->hk = item / a.RT;
-    p->rt = item - p->hk * a.RT;
-    p->len = len;
-    p->nt = nt;
-    p->t0 = static_cast<int>(off - static_cast<long>(item) * nt);
-    p->cnt = static_cast<int>(min(static_cast<long>(nt - p->t0), left));
-    off += p->cnt;
-    left -= p->cnt;
+    p.n = n;
+    p.hk = hk;
+    p.rt = rt;
+    p.len = len;
+    p.nt = nt;
+    p.t0 = t;
+    p.cnt = min(nt - t, left);
+    t += p.cnt;
+    left -= p.cnt;
     return true;
   }
 };
@@ -252,17 +306,25 @@ struct CacheRun {
 // The largest exponent among the part's V scales (one warp).
 __device__ __forceinline__ int part_vref(const CacheArgs& a, const CachePart& p, int lane) {
   const float* vs = a.v_scale + (static_cast<long>(p.n) * a.Hkv + p.hk) * (a.C / kCacheBlock);
-  const int b0 = 2 * p.t0, b1 = min(2 * (p.t0 + p.cnt), (p.len + kCacheBlock - 1) / kCacheBlock);
+  const int per = a.tile / kCacheBlock;
+  const int b0 = per * p.t0, b1 = min(per * (p.t0 + p.cnt), (p.len + kCacheBlock - 1) / kCacheBlock);
   int e = kCacheEMin;
   for (int b = b0 + lane; b < b1; b += 32) e = max(e, scale_exponent(vs[b]));
   return __reduce_max_sync(0xffffffffu, e);
 }
 
-// N scores of a thread (64, 32 or 16) from its lane of S: N columns from
+// N scores of a thread (64, 32, 16 or 8) from its lane of S: N columns from
 // `taddr` for half 0, N further on for half 1.
 template <int N>
 __device__ __forceinline__ void load_scores(uint32_t taddr, float (&s)[N]) {
-  if constexpr (N == 16) {
+  if constexpr (N == 8) {
+    uint32_t raw[8];
+    ptx::tmem_ld16x2<8>(taddr, raw);
+    ptx::tmem_wait_ld();
+    ptx::reg_fence8(raw);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) s[e] = __uint_as_float(raw[e]);
+  } else if constexpr (N == 16) {
     uint32_t raw[16];
     ptx::tmem_ld16x2<16>(taddr, raw);
     ptx::tmem_wait_ld();
@@ -283,14 +345,13 @@ __device__ __forceinline__ void load_scores(uint32_t taddr, float (&s)[N]) {
   }
 }
 
-// K: copies of a row tile in the accumulators' lanes (1, 2 or 4).
-template <int D, bool MOD, int K>
-__global__ void __launch_bounds__(512, 1)
+template <int D, bool MOD, int Q>
+__global__ void __launch_bounds__(CacheCfg<D, Q>::THREADS) __maxnreg__((CacheCfg<D, Q>::REGS_LAUNCH))
     cache_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                       const __grid_constant__ CacheArgs a) {
-  using C = CacheCfg<D>;
-  constexpr int COLS = C::BK / K;  // keys of a copy in a tile
-  constexpr int N = COLS / 2;      // keys of a thread
+  using C = CacheCfg<D, Q>;
+  constexpr bool FEW = C::FEW;
+  constexpr int N = C::N;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~static_cast<uintptr_t>(1023));
@@ -299,11 +360,15 @@ __global__ void __launch_bounds__(512, 1)
   const int lane = threadIdx.x & 31;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::OFF_MISC);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::OFF_MISC + 4);
-  volatile long* run_s = reinterpret_cast<volatile long*>(smem + C::OFF_MISC + 8);  // sequence, tile in it, tiles
+  volatile int* run_s = reinterpret_cast<volatile int*>(smem + C::OFF_MISC + 8);  // sequence, item in it, tile, tiles
   auto bar = [&](int idx) -> uint32_t { return sb + C::OFF_BAR + 8 * idx; };
 
   // ---- setup
   if (threadIdx.x == 0) {
+    for (int s = 0; s < C::WS; ++s) {
+      ptx::mbar_init(bar(C::B_WFULL + s), 4);
+      ptx::mbar_init(bar(C::B_WEMPTY + s), 1);
+    }
     for (int s = 0; s < C::KS; ++s) {
       ptx::mbar_init(bar(C::B_KFULL + s), 1);
       ptx::mbar_init(bar(C::B_KEMPTY + s), 1);
@@ -311,9 +376,9 @@ __global__ void __launch_bounds__(512, 1)
       ptx::mbar_init(bar(C::B_VEMPTY + s), 4);
     }
     for (int b = 0; b < 2; ++b) {
-      ptx::mbar_init(bar(C::B_WFULL + b), 4);
+        ptx::mbar_init(bar(C::B_SREAD + b), C::OWNERS);
       ptx::mbar_init(bar(C::B_SFULL + b), 1);
-      ptx::mbar_init(bar(C::B_PFULL + b), 8);
+      ptx::mbar_init(bar(C::B_PFULL + b), C::OWNERS);
       ptx::mbar_init(bar(C::B_PVDONE + b), 1);
       ptx::mbar_init(bar(C::B_DRAIN + b), 1);
       ptx::mbar_init(bar(C::B_QTFULL + b), 8);
@@ -335,7 +400,7 @@ __global__ void __launch_bounds__(512, 1)
     int n0 = a.N;
     for (int nb = 0; nb < a.N && begin < end; nb += 32) {
       const int n = nb + lane;
-      const long x = n < a.N ? static_cast<long>(cache_tiles(cache_len(a, n))) * a.Hkv * a.RT : 0;
+      const long x = n < a.N ? static_cast<long>(cache_tiles(a, cache_len(a, n))) * a.Hkv * a.RT : 0;
       long inc = x;
 #pragma unroll
       for (int off = 1; off < 32; off <<= 1) {
@@ -352,9 +417,13 @@ __global__ void __launch_bounds__(512, 1)
       base += __shfl_sync(0xffffffffu, inc, 31);
     }
     if (lane == 0) {
-      run_s[0] = n0 < a.N ? n0 : 0;
-      run_s[1] = begin - base;
-      run_s[2] = n0 < a.N ? end - begin : 0;
+      const bool some = n0 < a.N;
+      const int nt = some ? cache_tiles(a, cache_len(a, n0)) : 1;
+      const long off = begin - base;
+      run_s[0] = some ? n0 : 0;
+      run_s[1] = some ? static_cast<int>(off / nt) : 0;
+      run_s[2] = some ? static_cast<int>(off % nt) : 0;
+      run_s[3] = some ? static_cast<int>(end - begin) : 0;
     }
   }
   ptx::tc_fence_before();
@@ -362,16 +431,32 @@ __global__ void __launch_bounds__(512, 1)
   ptx::tc_fence_after();
   ptx::grid_dep_launch();
   const uint32_t tmem = *tmem_slot;
+  if constexpr (FEW) {
+    // P: all zero; from here on a copy writes its own keys only
+    if (warp < 4) {
+      uint32_t zero[32];
+#pragma unroll
+      for (int e = 0; e < 32; ++e) zero[e] = 0u;
+      ptx::tmem_st32(tmem + (static_cast<uint32_t>(warp * 32) << 16) + C::TM_P0, zero);
+      ptx::tmem_st32(tmem + (static_cast<uint32_t>(warp * 32) << 16) + C::TM_P1, zero);
+      ptx::tmem_wait_st();
+    }
+    ptx::tc_fence_before();
+    __syncthreads();
+    ptx::tc_fence_after();
+  }
   CacheRun run;
-  run.n = static_cast<int>(run_s[0]);
-  run.off = run_s[1];
-  run.left = run_s[2];
+  run.n = run_s[0];
+  run.hk = run_s[1] / a.RT;
+  run.rt = run_s[1] - run.hk * a.RT;
+  run.t = run_s[2];
+  run.left = run_s[3];
   if (run.left > 0) run.load(a);
   CachePart part;
 
   if (warp >= 12) {
     // ================================================================ widen V
-    ptx::setmaxnreg_dec_88();
+    ptx::setmaxnreg_dec<C::REGS_WIDEN>();
     const int tid = threadIdx.x - 384;
     constexpr int TPR = D / 16;            // threads of a row, 16 values each
     constexpr int ROWS = 128 / TPR;        // rows of a pass
@@ -387,48 +472,54 @@ __global__ void __launch_bounds__(512, 1)
     const uint32_t off_b = row0 * 128 + (((2 * (j & 3) + (sw ? 0 : 1)) ^ swz) << 4) + chunk * (C::BK * 128);
     int g = 0;
     bool ok = true;
-    while (ok && run.next(a, &part)) {
+    while (ok && run.next(a, part)) {
       const int vref = part_vref(a, part, lane);
       const float* vs = a.v_scale + (static_cast<long>(part.n) * a.Hkv + part.hk) * (a.C / kCacheBlock);
       const int last = a.C / kCacheBlock - 1;
-      // the next tile's scales are read a tile ahead
-      float sc0 = vs[2 * part.t0], sc1 = vs[min(2 * part.t0 + 1, last)];
-      for (int t = part.t0; t < part.t0 + part.cnt; ++t, ++g) {
-        const int st = g % C::VS, b = g & 1;
-        const int valid = part.len - t * C::BK;
-        // 2^(ev - vref) of both scale blocks as f16 pairs (0 below f16's range,
-        // which includes a block past the length: its rows are cleared)
-        uint32_t mul[2];
+      constexpr int PER = C::BK / kCacheBlock;  // scale blocks of a tile
+      // a tile's scales are read a tile ahead
+      const int t_last = part.t0 + part.cnt - 1;
+      float sc[PER];
 #pragma unroll
-        for (int x = 0; x < 2; ++x) {
-          const int dlt = min(scale_exponent(x ? sc1 : sc0) - vref, 0);
+      for (int x = 0; x < PER; ++x) sc[x] = vs[min(PER * t_last + x, last)];
+      for (int t = t_last; t >= part.t0; --t, ++g) {
+        const int st = g % C::KS, ws = g % C::WS;
+        const int valid = part.len - t * C::BK;
+        // 2^(ev - vref) as f16 pairs (0 below f16's range; a block past the
+        // length may hold any scale: its rows are cleared)
+        uint32_t mul[PER];
+#pragma unroll
+        for (int x = 0; x < PER; ++x) {
+          const int dlt = min(scale_exponent(sc[x]) - vref, 0);
           const uint32_t hbits = dlt >= -14 ? static_cast<uint32_t>(dlt + 15) << 10
                                             : (dlt >= -24 ? 1u << (dlt + 24) : 0u);
           mul[x] = hbits | (hbits << 16);
+          if (t > part.t0) sc[x] = vs[PER * (t - 1) + x];
         }
-        if (t + 1 < part.t0 + part.cnt) {
-          sc0 = vs[2 * t + 2];
-          sc1 = vs[min(2 * t + 3, last)];
-        }
-        if (!ptx::mbar_wait_warp(bar(C::B_VFULL + st), (g / C::VS) & 1, abort_flag, a.timeout_ns, kErrTimeout) ||
-            (g >= 2 &&
-             !ptx::mbar_wait_warp(bar(C::B_PVDONE + b), ((g - 2) >> 1) & 1, abort_flag, a.timeout_ns, kErrTimeout))) {
+        if (!ptx::mbar_wait_warp(bar(C::B_VFULL + st), (g / C::KS) & 1, abort_flag, a.timeout_ns, kErrTimeout)) {
           ok = false;
           break;
         }
         const uint8_t* src = smem + C::OFF_V + st * C::T8 + row0 * D + j * 16;
-        uint8_t* dst = smem + C::OFF_W + b * C::T16;
+        uint8_t* dst = smem + C::OFF_W + ws * C::T16;
         uint4 x[NP];
 #pragma unroll
         for (int p = 0; p < NP; ++p) x[p] = *reinterpret_cast<const uint4*>(src + p * (ROWS * D));
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(bar(C::B_VEMPTY + st));
         if (valid < C::BK) {
 #pragma unroll
           for (int p = 0; p < NP; ++p)
             if (row0 + p * ROWS >= valid) x[p] = make_uint4(0, 0, 0, 0);
         }
+        if (g >= C::WS &&
+            !ptx::mbar_wait_warp(bar(C::B_WEMPTY + ws), (g / C::WS - 1) & 1, abort_flag, a.timeout_ns, kErrTimeout)) {
+          ok = false;
+          break;
+        }
 #pragma unroll
         for (int p = 0; p < NP; ++p) {
-          const uint32_t m2 = mul[p >= NP / 2 ? 1 : 0];
+          const uint32_t m2 = mul[p * PER / NP];
           const uint32_t w[4] = {sw ? x[p].z : x[p].x, sw ? x[p].w : x[p].y, sw ? x[p].x : x[p].z, sw ? x[p].y : x[p].w};
           uint32_t h[8];
 #pragma unroll
@@ -445,14 +536,11 @@ __global__ void __launch_bounds__(512, 1)
         }
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         __syncwarp();
-        if (lane == 0) {
-          ptx::mbar_arrive(bar(C::B_WFULL + b));
-          ptx::mbar_arrive(bar(C::B_VEMPTY + st));
-        }
+        if (lane == 0) ptx::mbar_arrive(bar(C::B_WFULL + ws));
       }
     }
   } else if (warp >= 8) {
-    setmaxnreg_dec_56();
+    ptx::setmaxnreg_dec<C::REGS_CONTROL>();
     const uint32_t leader = ptx::elect_one();
     auto wait = [&](int idx, int parity) -> bool {
       return ptx::mbar_wait_warp(bar(idx), parity & 1, abort_flag, a.timeout_ns, kErrTimeout);
@@ -465,9 +553,9 @@ __global__ void __launch_bounds__(512, 1)
       }
       int g = 0, issued_k = 0, issued_v = 0;
       bool ok = true;
-      while (ok && run.next(a, &part)) {
+      while (ok && run.next(a, part)) {
         const int z = part.n * a.Hkv + part.hk;
-        for (int t = part.t0; t < part.t0 + part.cnt; ++t, ++g) {
+        for (int t = part.t0 + part.cnt - 1; t >= part.t0; --t, ++g) {
           const int st = g % C::KS;
           if (g >= C::KS && !wait(C::B_KEMPTY + st, g / C::KS - 1)) {
             ok = false;
@@ -476,7 +564,7 @@ __global__ void __launch_bounds__(512, 1)
           ptx::mbar_arrive_expect_tx_if(leader, bar(C::B_KFULL + st), C::T8);
           ptx::tma_load_3d_if(leader, sb + C::OFF_K + st * C::T8, &tm_k, bar(C::B_KFULL + st), 0, t * C::BK, z);
           issued_k = g + 1;
-          if (g >= C::VS && !wait(C::B_VEMPTY + st, g / C::VS - 1)) {
+          if (g >= C::KS && !wait(C::B_VEMPTY + st, g / C::KS - 1)) {
             ok = false;
             break;
           }
@@ -491,8 +579,8 @@ __global__ void __launch_bounds__(512, 1)
         volatile int dummy = 0;
         for (int u = (issued_k > C::KS ? issued_k - C::KS : 0); u < issued_k; ++u)
           ptx::mbar_wait(bar(C::B_KFULL + u % C::KS), (u / C::KS) & 1, &dummy, short_ns, 0);
-        for (int u = (issued_v > C::VS ? issued_v - C::VS : 0); u < issued_v; ++u)
-          ptx::mbar_wait(bar(C::B_VFULL + u % C::VS), (u / C::VS) & 1, &dummy, short_ns, 0);
+        for (int u = (issued_v > C::KS ? issued_v - C::KS : 0); u < issued_v; ++u)
+          ptx::mbar_wait(bar(C::B_VFULL + u % C::KS), (u / C::KS) & 1, &dummy, short_ns, 0);
         __syncwarp();
       }
     } else if (warp == 9) {
@@ -500,7 +588,7 @@ __global__ void __launch_bounds__(512, 1)
       const uint32_t klo = ptx::sdesc_sw128_lo(sb + C::OFF_K, 16);
       int g = 0, iq = 0;
       bool ok = true;
-      while (ok && run.next(a, &part)) {
+      while (ok && run.next(a, part)) {
         const int qc = iq & 1;
         if (!wait(C::B_QTFULL + qc, iq >> 1)) {
           ok = false;
@@ -509,7 +597,9 @@ __global__ void __launch_bounds__(512, 1)
         const uint32_t q_tmem = tmem + (qc ? C::TM_Q1 : C::TM_Q0);
         for (int t = 0; t < part.cnt; ++t, ++g) {
           const int b = g & 1, st = g % C::KS;
-          if (!wait(C::B_KFULL + st, g / C::KS) || (g >= 2 && !wait(C::B_PVDONE + b, (g - 2) >> 1))) {
+          // S_b is free once it has been read (few rows), or PV has read the P over it
+          if (!wait(C::B_KFULL + st, g / C::KS) ||
+              (g >= 2 && !wait((FEW ? C::B_SREAD : C::B_PVDONE) + b, (g - 2) >> 1))) {
             ok = false;
             break;
           }
@@ -541,21 +631,22 @@ __global__ void __launch_bounds__(512, 1)
       const uint32_t vlo = ptx::sdesc_sw128_lo(sb + C::OFF_W, C::BK * 128);
       int g = 0;
       bool ok = true;
-      while (ok && run.next(a, &part)) {
+      while (ok && run.next(a, part)) {
         for (int t = 0; t < part.cnt; ++t, ++g) {
-          const int b = g & 1;
-          if (!wait(C::B_WFULL + b, g >> 1) || !wait(C::B_PFULL + b, g >> 1)) {
+          const int b = g & 1, ws = g % C::WS;
+          if (!wait(C::B_WFULL + ws, g / C::WS) || !wait(C::B_PFULL + b, g >> 1)) {
             ok = false;
             break;
           }
           ptx::tc_fence_after();
-          const uint32_t b0 = vlo + static_cast<uint32_t>(b * C::T16 >> 4);
-          const uint32_t p_tmem = tmem + (b ? C::TM_S1 : C::TM_S0);
+          const uint32_t b0 = vlo + static_cast<uint32_t>(ws * C::T16 >> 4);
+          const uint32_t p_tmem = tmem + (b ? C::TM_P1 : C::TM_P0);
 #pragma unroll
           for (int kk = 0; kk < C::BK / 16; ++kk)
             ptx::umma_ts_lohi_if(leader, tmem + C::TM_O, p_tmem + kk * 8, b0 + kk * (2048 >> 4), HI, C::IDESC_PV,
                                  (t > 0 || kk > 0) ? 1u : 0u);
           ptx::umma_commit_if(leader, bar(C::B_PVDONE + b));
+          ptx::umma_commit_if(leader, bar(C::B_WEMPTY + ws));
         }
       }
       if (!ok) {
@@ -567,15 +658,16 @@ __global__ void __launch_bounds__(512, 1)
     }
   } else {
     // ================================================================ softmax
-    ptx::setmaxnreg_inc_184();
+    ptx::setmaxnreg_inc<C::REGS_SOFTMAX>();
     const int half = lane >> 4;
     const int quad = warp & 3, hw = warp >> 2;
-    // lanes 16*hw.. of a quad hold the 16 rows of block rb for copy `copy`
-    const int copy = K == 1 ? 0 : (K == 2 ? hw : quad);
-    const int rb = K == 1 ? 2 * quad + hw : (K == 2 ? quad : hw);
+    // lanes 16*hw.. of quarter `quad` hold the 16 rows of block rb, for the
+    // tiles of parity hw and part `copy` of their keys (few rows)
+    const int rb = Q == 0 ? 2 * quad + hw : (Q == 1 ? quad : (Q == 2 ? (quad & 1) : 0));
+    const int copy = Q <= 1 ? 0 : (Q == 2 ? quad >> 1 : quad);
     const int r = rb * 16 + (lane & 15);           // my row
-    const int key0 = copy * COLS + half * N;       // my first key of a tile
-    const int sblk = key0 / kCacheBlock;           // ... its scale block
+    const int key0 = copy * C::COLS + half * N;    // my first key of a tile
+    const int sblk = key0 / kCacheBlock;           // ... its scale block in the tile
     const uint32_t lane_base = tmem + (static_cast<uint32_t>(quad * 32 + hw * 16) << 16);
     const float ninf = -__int_as_float(0x7f800000);
     uint64_t cap[5];
@@ -583,98 +675,239 @@ __global__ void __launch_bounds__(512, 1)
 #pragma unroll
       for (int u = 0; u < 5; ++u) cap[u] = ptx::f32x2(a.cap_c[u], a.cap_c[u]);
     }
-    int cq = 0;  // Q copies so far
-    // Q of a part into TMEM Q_{cq&1}, hi and lo; returns my row's exponent.
-    // Warp w copies half w/4 of the elements of the rows in lanes 32*(w%4) + lane.
-    int eq_new = 0;
-    auto copy_q = [&](const CachePart& p) -> bool {
-      const int c = cq & 1;
-      const int rows = min(128, a.R - p.rt * 128);
-      const int qr = K == 1 ? quad * 32 + lane : (K == 2 ? quad * 16 + (lane & 15) : lane);
-      uint32_t mx = 0;
-      const uint16_t* src = nullptr;
-      const bool quad_on = __any_sync(0xffffffffu, qr < rows);
-      if (quad_on) {
-        const int rr = p.rt * 128 + min(qr, rows - 1);
-        const int hg = rr / a.B, tb = rr - hg * a.B;
-        src = a.q + p.n * a.qs_n + (static_cast<size_t>(p.hk) * a.group + hg) * a.qs_h + tb * a.qs_b;
-        // the whole row for its maximum; my half is read again below (from L1)
-#pragma unroll 8
-        for (int u = 0; u < D / 8; ++u) {
-          const uint4 x = qr < rows ? *reinterpret_cast<const uint4*>(src + u * 8) : make_uint4(0, 0, 0, 0);
-          const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const uint32_t lo = w[e] & 0x7FFFu, hi = (w[e] >> 16) & 0x7FFFu;
-            mx = max(mx, lo < 0x7F80u ? lo : 0u);
-            mx = max(mx, hi < 0x7F80u ? hi : 0u);
-          }
-        }
-      }
-      const int e = exponent_for(mx);
-      if (cq >= 2 &&
-          !ptx::mbar_wait_warp(bar(C::B_QTEMPTY + c), ((cq >> 1) - 1) & 1, abort_flag, a.timeout_ns, kErrTimeout))
-        return false;
-      ptx::tc_fence_after();
-      if (quad_on) {
-        const float inv = pow2i(-e);
-        uint32_t hi4[D / 8], lo4[D / 8];  // my half: D/2 elements, four to a word
-#pragma unroll
-        for (int u = 0; u < D / 16; ++u) {
-          const uint4 v =
-              qr < rows ? *reinterpret_cast<const uint4*>(src + hw * (D / 2) + u * 8) : make_uint4(0, 0, 0, 0);
-          float f[8];
-          bf16x8_to_f32(v, f);
-#pragma unroll
-          for (int k = 0; k < 8; ++k) {
-            f[k] *= inv;
-            if (fabsf(f[k]) == __int_as_float(0x7f800000)) f[k] = __int_as_float(0x7fffffff);  // inf has no e4m3
-          }
-#pragma unroll
-          for (int k = 0; k < 2; ++k) {
-            const uint32_t h0 = pack_e4m3x2(f[4 * k], f[4 * k + 1]), h1 = pack_e4m3x2(f[4 * k + 2], f[4 * k + 3]);
-            float g0, g1, g2, g3;
-            unpack_e4m3x2(h0, g0, g1);
-            unpack_e4m3x2(h1, g2, g3);
-            hi4[2 * u + k] = h0 | (h1 << 16);
-            lo4[2 * u + k] = pack_e4m3x2(f[4 * k] - g0, f[4 * k + 1] - g1) |
-                             (pack_e4m3x2(f[4 * k + 2] - g2, f[4 * k + 3] - g3) << 16);
-          }
-        }
-        const uint32_t qa = tmem + (static_cast<uint32_t>(quad * 32) << 16) + (c ? C::TM_Q1 : C::TM_Q0) + hw * (D / 8);
-        if constexpr (D == 128) {
-          ptx::tmem_st32_16(qa, hi4);
-          ptx::tmem_st32_16(qa + D / 4, lo4);
-        } else {
-          ptx::tmem_st32_8(qa, hi4);
-          ptx::tmem_st32_8(qa + D / 4, lo4);
-        }
-        ptx::tmem_wait_st();
-      }
-      ptx::tc_fence_before();
-      eq_new = __shfl_sync(0xffffffffu, e, hw * 16 + (lane & 15));
-      __syncwarp();
-      if (lane == 0) ptx::mbar_arrive(bar(C::B_QTFULL + c));
-      ++cq;
-      return true;
-    };
     int g = 0;
     int joins = 0;  // phases of B_JOIN
     bool ok = true;
-    // every softmax warp has come here (K > 1: copies exchange through shared memory)
+    // every softmax warp has come here (the copies exchange through shared memory)
     auto join = [&]() -> bool {
       __syncwarp();
       if (lane == 0) ptx::mbar_arrive(bar(C::B_JOIN));
       return ptx::mbar_wait_warp(bar(C::B_JOIN), joins++ & 1, abort_flag, a.timeout_ns, kErrTimeout);
     };
+    int cq = 0;      // Q copies so far
+    int eq_new = 0;  // the last copy's exponent of my row
+    // Q of a part into TMEM Q_{cq&1}, hi and lo. First each row by D/8 threads of
+    // eight elements: its largest exponent, hi and lo, into shared memory (16-byte
+    // units permuted by the row). Then warp w takes the half w/4 of the rows in
+    // lanes 32*(w%4) + lane. Rows past the last are zero.
+    auto copy_q = [&](const CachePart& p) -> bool {
+      constexpr int TPR = D / 8, RPP = 256 / TPR, NP = (C::ROWS + RPP - 1) / RPP, UNITS = D / 16;
+      const int c = cq & 1;
+      const int rows = min(128, a.R - p.rt * 128);
+      const int ch = threadIdx.x % TPR, row0 = threadIdx.x / TPR;
+      uint8_t* stage = smem + C::OFF_Q;
+      int* eqs = reinterpret_cast<int*>(stage + 2 * C::ROWS * D);
+      const uint16_t* qn = a.q + p.n * a.qs_n + static_cast<size_t>(p.hk) * a.group * a.qs_h + ch * 8;
+      uint4 x[NP < 4 ? NP : 4];
+      bool joined = false;
+#pragma unroll 1
+      for (int base = 0; base < NP; base += 4) {
+#pragma unroll
+        for (int u = 0; u < (NP < 4 ? NP : 4); ++u) {
+          const int row = row0 + (base + u) * RPP, rr = p.rt * 128 + row;
+          const int hg = rr / a.B;
+          x[u] = row < rows ? *reinterpret_cast<const uint4*>(qn + hg * a.qs_h + (rr - hg * a.B) * a.qs_b)
+                            : make_uint4(0, 0, 0, 0);
+        }
+        if (!joined) {  // the last copy has been read
+          if (!join()) return false;
+          joined = true;
+        }
+#pragma unroll
+        for (int u = 0; u < (NP < 4 ? NP : 4); ++u) {
+          const int row = row0 + (base + u) * RPP;
+          const uint32_t w[4] = {x[u].x, x[u].y, x[u].z, x[u].w};
+          uint32_t mx = 0;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) mx = max(mx, max(w[e] & 0x7FFFu, (w[e] >> 16) & 0x7FFFu));
+#pragma unroll
+          for (int off = TPR / 2; off > 0; off >>= 1) mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, off));
+          // a row with an infinity or NaN becomes NaN whatever its exponent
+          const int e = exponent_for(min(mx, 0x7F7Fu));
+          const float inv = pow2i(-e);
+          float f[8];
+          bf16x8_to_f32(x[u], f);
+          uint32_t hi[4], lo[4];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            float f0 = f[2 * k] * inv, f1 = f[2 * k + 1] * inv;
+            // infinity has no e4m3
+            if (fabsf(f0) == __int_as_float(0x7f800000)) f0 = __int_as_float(0x7fffffff);
+            if (fabsf(f1) == __int_as_float(0x7f800000)) f1 = __int_as_float(0x7fffffff);
+            hi[k] = pack_e4m3x2(f0, f1);
+            float g0, g1;
+            unpack_e4m3x2(hi[k], g0, g1);
+            lo[k] = pack_e4m3x2(f0 - g0, f1 - g1);
+          }
+          if (row < C::ROWS) {
+            uint8_t* dst = stage + row * D + (((ch >> 1) ^ (row & (UNITS - 1))) << 4) + (ch & 1) * 8;
+            *reinterpret_cast<uint2*>(dst) = make_uint2(hi[0] | (hi[1] << 16), hi[2] | (hi[3] << 16));
+            *reinterpret_cast<uint2*>(dst + C::ROWS * D) = make_uint2(lo[0] | (lo[1] << 16), lo[2] | (lo[3] << 16));
+            if (ch == 0) eqs[row] = e;
+          }
+        }
+      }
+      if (!join()) return false;
+      if (cq >= 2 &&
+          !ptx::mbar_wait_warp(bar(C::B_QTEMPTY + c), ((cq >> 1) - 1) & 1, abort_flag, a.timeout_ns, kErrTimeout))
+        return false;
+      ptx::tc_fence_after();
+      const int qr = Q == 0 ? quad * 32 + lane : rb * 16 + (lane & 15);
+      const uint32_t qa = tmem + (static_cast<uint32_t>(quad * 32) << 16) + (c ? C::TM_Q1 : C::TM_Q0) + hw * (D / 8);
+#pragma unroll
+      for (int part2 = 0; part2 < 2; ++part2) {  // hi, lo
+        uint32_t v[D / 8];
+#pragma unroll
+        for (int u = 0; u < D / 32; ++u) {
+          const uint4 y = *reinterpret_cast<const uint4*>(stage + part2 * C::ROWS * D + qr * D +
+                                                          (((hw * (D / 32) + u) ^ (qr & (UNITS - 1))) << 4));
+          v[4 * u] = y.x;
+          v[4 * u + 1] = y.y;
+          v[4 * u + 2] = y.z;
+          v[4 * u + 3] = y.w;
+        }
+        if constexpr (D == 128) ptx::tmem_st32_16(qa + part2 * (D / 4), v);
+        else ptx::tmem_st32_8(qa + part2 * (D / 4), v);
+      }
+      eq_new = eqs[r];
+      ptx::tmem_wait_st();
+      ptx::tc_fence_before();
+      __syncwarp();
+      if (lane == 0) ptx::mbar_arrive(bar(C::B_QTFULL + c));
+      ++cq;
+      return true;
+    };
+    // One turn: the next part's Q goes into TMEM, so that its S MMAs start while
+    // the last part is written out; then that part's epilogue, then the tiles.
     CachePart nextp;
-    bool have = run.next(a, &nextp);
-    if (have && !copy_q(nextp)) ok = false;
-    while (ok && have) {
+    bool have = false;  // a part's tiles are done and wait for their epilogue
+    int rows = 0, vref = 0;
+    bool warp_on = false;
+    float m = ninf, l = 0.f;
+    while (ok) {
+      const bool more = run.next(a, nextp);
+      if (more && !copy_q(nextp)) {
+        ok = false;
+        break;
+      }
+      if (have) {
+        // ---- epilogue
+        if (!ptx::mbar_wait_warp(bar(C::B_PVDONE + ((g - 1) & 1)), ((g - 1) >> 1) & 1, abort_flag, a.timeout_ns,
+                                 kErrTimeout)) {
+          ok = false;
+          break;
+        }
+        ptx::tc_fence_after();
+        const bool row_valid = r < rows;
+        const float lt = l + __shfl_xor_sync(0xffffffffu, l, 16);
+        const bool whole = part.cnt == part.nt;
+        const long grow0 = (static_cast<long>(part.n) * a.Hkv + part.hk) * a.R + part.rt * 128;
+        const long prow0 = static_cast<long>(2 * blockIdx.x + (part.t0 == 0 ? 1 : 0)) * a.part_rows;
+        // sums of my row over all copies, of which mine is number cc
+        constexpr int K = FEW ? 2 * Q : 1, RB = FEW ? 4 / Q : 8;  // copies, row blocks
+        const int cc = hw * Q + copy;
+        float M = m, L = lt;
+        if constexpr (FEW) {
+          float2* ml = reinterpret_cast<float2*>(smem + C::OFF_J + C::J_BYTES);  // [copy][row]
+          if (half == 0) ml[(cc * RB + rb) * 16 + (lane & 15)] = make_float2(m, lt);
+          if (!join()) {
+            ok = false;
+            break;
+          }
+          M = ninf;
+          L = 0.f;
+          if (warp_on) {
+#pragma unroll
+            for (int o = 0; o < K; ++o) M = fmaxf(M, ml[(o * RB + rb) * 16 + (lane & 15)].x);
+#pragma unroll
+            for (int o = 0; o < K; ++o) {
+              const float2 x = ml[(o * RB + rb) * 16 + (lane & 15)];
+              L += x.y == 0.f ? 0.f : x.y * ptx::ex2(x.x - M);
+            }
+          }
+        }
+        const bool empty = L == 0.f;
+        // a copy that saw no key left m at -inf and its O at zero
+        const float share = !FEW || m == M ? 1.f : (m == ninf ? 0.f : ptx::ex2(m - M));
+        const float f = (empty ? 0.f : share / L) * pow2i(vref);
+        if (row_valid && half == 0 && (!FEW || cc == 0)) {
+          const float lse2 = empty ? ninf : M - kPShift + ptx::lg2(L);
+          if (whole) a.lse[grow0 + r] = lse2 * 0.69314718055994530942f;
+          else a.l_part[prow0 + r] = lse2;
+        }
+#pragma unroll 1
+        for (int c = 0; c < D / 64; ++c) {
+          float v[32];
+          if (warp_on) {
+            uint32_t raw[32];
+            ptx::tmem_ld16x2_32<D / 2>(lane_base + C::TM_O + c * 32, raw);
+            ptx::tmem_wait_ld();
+            ptx::reg_fence32(raw);
+#pragma unroll
+            for (int e = 0; e < 32; ++e) v[e] = f == 0.f ? 0.f : __uint_as_float(raw[e]) * f;
+          }
+          if constexpr (!FEW) {
+            if (row_valid) {
+              uint4* o_dst = reinterpret_cast<uint4*>(a.o + (grow0 + r) * D) + half * (D / 16) + c * 4;
+              float4* p_dst = reinterpret_cast<float4*>(a.o_part + (prow0 + r) * D) + half * (D / 8) + c * 8;
+              if (whole) {
+#pragma unroll
+                for (int u = 0; u < 4; ++u)
+                  o_dst[u] = make_uint4(ptx::pack_bf16x2(v[8 * u], v[8 * u + 1]), ptx::pack_bf16x2(v[8 * u + 2], v[8 * u + 3]),
+                                        ptx::pack_bf16x2(v[8 * u + 4], v[8 * u + 5]), ptx::pack_bf16x2(v[8 * u + 6], v[8 * u + 7]));
+              } else {
+#pragma unroll
+                for (int u = 0; u < 8; ++u) p_dst[u] = make_float4(v[4 * u], v[4 * u + 1], v[4 * u + 2], v[4 * u + 3]);
+              }
+            }
+          } else {
+            // [copy][row][16 float4], the float4 of a row permuted by the row
+            float4* jb = reinterpret_cast<float4*>(smem + C::OFF_J);
+            if (c > 0 && !join()) {  // the previous columns have been read
+              ok = false;
+              break;
+            }
+            if (warp_on) {
+              float4* dst = jb + ((cc * RB + rb) * 16 + (lane & 15)) * 16;
+#pragma unroll
+              for (int u = 0; u < 8; ++u)
+                dst[(half * 8 + u) ^ (lane & 15)] = make_float4(v[4 * u], v[4 * u + 1], v[4 * u + 2], v[4 * u + 3]);
+            }
+            if (!join()) {
+              ok = false;
+              break;
+            }
+            const int tid = threadIdx.x;  // 0..255
+            for (int x = tid; x < rows * 16; x += 256) {
+              const int row = x >> 4, u = x & 15;
+              float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+              for (int o = 0; o < K; ++o) {
+                const float4 y = jb[(o * RB * 16 + row) * 16 + (u ^ (row & 15))];
+                sum.x += y.x;
+                sum.y += y.y;
+                sum.z += y.z;
+                sum.w += y.w;
+              }
+              // element: half u/8 of the row, 32 columns of this pass
+              const int e = (u >> 3) * (D / 2) + c * 32 + (u & 7) * 4;
+              if (whole)
+                *reinterpret_cast<uint2*>(a.o + (grow0 + row) * D + e) =
+                    make_uint2(ptx::pack_bf16x2(sum.x, sum.y), ptx::pack_bf16x2(sum.z, sum.w));
+              else
+                *reinterpret_cast<float4*>(a.o_part + (prow0 + row) * D + e) = sum;
+            }
+          }
+        }
+        if (!ok) break;
+        // the next part's first PV overwrites O only after this warp's next PFULL
+        // arrival (few rows: after the last join), which follows the loads above
+      }
+      if (!more) break;
       part = nextp;
-      const int rows = min(128, a.R - part.rt * 128);
-      const bool warp_on = rb * 16 < rows;
-      const bool row_valid = r < rows;
+      have = true;
+      rows = min(128, a.R - part.rt * 128);
+      warp_on = rb * 16 < rows;
       const long sbase = (static_cast<long>(part.n) * a.Hkv + part.hk) * (a.C / kCacheBlock);
       const float qmul = pow2i(eq_new);
       float slope2 = 0.f;
@@ -685,27 +918,39 @@ __global__ void __launch_bounds__(512, 1)
         if (a.slopes) slope2 = a.slopes[part.hk * a.group + hg] * 1.44269504088896340736f;
         at = (a.q_start ? min(max(a.q_start[part.n], -(1 << 29)), 1 << 29) : part.len - a.B) + (rr - hg * a.B);
       }
-      float m = ninf, l = 0.f;
+      m = ninf;
+      l = 0.f;
+      // <q, k> from the scaled operands; the factor stays finite
       auto scale_of = [&](int t) -> float {
-        const int blk = min(2 * t + sblk, a.C / kCacheBlock - 1);
+        const int blk = min(t * (C::BK / kCacheBlock) + sblk, a.C / kCacheBlock - 1);
         return warp_on ? a.k_scale[sbase + blk] : 1.f;
       };
-      float ks_next = scale_of(part.t0);
-      const int vref = part_vref(a, part, lane);
-      for (int jj = 0; jj < part.cnt; ++jj, ++g) {
-        const int t = part.t0 + jj, b = g & 1;
-        const float ks = ks_next;
-        if (jj + 1 < part.cnt) ks_next = scale_of(t + 1);
+      // my tiles: all, or those of parity hw; a tile's scale is read a tile ahead
+      const int t_last = part.t0 + part.cnt - 1;
+      const int skip = FEW ? ((g ^ hw) & 1) : 0;
+      constexpr int STEP = FEW ? 2 : 1;
+      const int g_part = g;
+      float ks_next = scale_of(max(t_last - skip, 0));
+      bool fresh = true;  // no tile of this part yet
+      vref = part_vref(a, part, lane);
+      for (int jj = skip; jj < part.cnt; jj += STEP) {
+        g = g_part + jj;
+        const int t = t_last - jj, b = g & 1;
+        const float f2 = fminf(qmul * pow2i(scale_exponent(ks_next)), 1e37f);
+        if (t >= part.t0 + STEP) ks_next = scale_of(t - STEP);
         if (!ptx::mbar_wait_warp(bar(C::B_SFULL + b), (g >> 1) & 1, abort_flag, a.timeout_ns, kErrTimeout)) {
           ok = false;
           break;
         }
         ptx::tc_fence_after();
+        float s[N];
+        if (warp_on) load_scores<N>(lane_base + (b ? C::TM_S1 : C::TM_S0) + copy * C::COLS, s);
+        if constexpr (FEW) {
+          ptx::tc_fence_before();
+          __syncwarp();
+          if (lane == 0) ptx::mbar_arrive(bar(C::B_SREAD + b));
+        }
         if (warp_on) {
-          float s[N];
-          load_scores<N>(lane_base + (b ? C::TM_S1 : C::TM_S0) + copy * COLS, s);
-          // <q, k> from the scaled operands; the factor stays finite
-          const float f2 = fminf(qmul * pow2i(scale_exponent(ks)), 1e37f);
           float f = fminf(f2 * a.scale_log2, 1e37f);
           const int valid = part.len - t * C::BK - key0;
           if constexpr (MOD) {
@@ -731,19 +976,12 @@ __global__ void __launch_bounds__(512, 1)
                   ptx::f32x2_split(mul_f32x2(v, cap_poly(v, cap)), s[c], s[c + 1]);
                 }
               }
-            } else {
-              const float ff = fminf(f2 * a.scale_log2, 1e37f);
-              const uint64_t f22 = ptx::f32x2(ff, ff);
-#pragma unroll
-              for (int c = 0; c < N; c += 2)
-                ptx::f32x2_split(mul_f32x2(ptx::f32x2(s[c], s[c + 1]), f22), s[c], s[c + 1]);
             }
+            const float ff = a.capped ? 1.f : fminf(f2 * a.scale_log2, 1e37f);
             if (a.slopes) {
-              // a thread's keys against its own row: one side or around it
-              const int c0 = t * C::BK + key0;
-              const bool around = __any_sync(0xffffffffu, at > c0 && at < c0 + N - 1);
-              if (around) add_bias(s, slope2, at, c0, 0);
-              else add_bias(s, slope2, at, c0, at <= c0 ? 1 : -1);
+              scale_and_bias(s, ff, slope2, at, t * C::BK + key0);
+            } else if (!a.capped) {
+              f = ff;
             }
           }
           if (valid < N) {
@@ -754,9 +992,11 @@ __global__ void __launch_bounds__(512, 1)
           float mx = row_max(s) * f;
           mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
           const float m_new = fmaxf(m, mx);
-          if (jj == 0) {
+          if (fresh) {
             m = m_new;
+            fresh = false;
           } else if (__any_sync(0xffffffffu, m_new > m + 8.0f)) {
+            // every PV before this tile's is complete, and this one's waits for me
             if (!ptx::mbar_wait_warp(bar(C::B_PVDONE + ((g - 1) & 1)), ((g - 1) >> 1) & 1, abort_flag, a.timeout_ns,
                                      kErrTimeout)) {
               ok = false;
@@ -782,28 +1022,34 @@ __global__ void __launch_bounds__(512, 1)
           const uint64_t f2x = ptx::f32x2(f, f), neg2 = ptx::f32x2(neg, neg);
           uint64_t acc0 = ptx::f32x2(0.f, 0.f), acc1 = acc0;
           uint32_t pk[N / 2];
+          // with a steep bias whole tiles lie where 2^x is exactly 0
+          if (MOD && !__any_sync(0xffffffffu, !(mx + neg < -127.f))) {
 #pragma unroll
-          for (int e = 0; e < N / 2; ++e) {
-            float x0, x1;
-            ptx::f32x2_split(ptx::fma_f32x2(ptx::f32x2(s[2 * e], s[2 * e + 1]), f2x, neg2), x0, x1);
-            const float p0 = ptx::ex2(x0), p1 = ptx::ex2(x1);
-            if (e & 1) acc1 = ptx::add_f32x2(acc1, ptx::f32x2(p0, p1));
-            else acc0 = ptx::add_f32x2(acc0, ptx::f32x2(p0, p1));
-            pk[e] = ptx::pack_f16x2(p0, p1);
-          }
-          const uint32_t p_taddr = lane_base + (b ? C::TM_S1 : C::TM_S0);
-          ptx::tmem_st16x2<N / 2>(p_taddr + copy * (COLS / 2), pk);
-          if constexpr (K > 1) {  // my lanes' P of the other copies' keys
-            uint32_t zero[N / 2];
+            for (int e = 0; e < N / 2; ++e) pk[e] = 0u;
+          } else {
 #pragma unroll
-            for (int e = 0; e < N / 2; ++e) zero[e] = 0u;
-#pragma unroll
-            for (int o = 1; o < K; ++o) ptx::tmem_st16x2<N / 2>(p_taddr + ((copy + o) % K) * (COLS / 2), zero);
+            for (int e = 0; e < N / 2; ++e) {
+              float x0, x1;
+              ptx::f32x2_split(ptx::fma_f32x2(ptx::f32x2(s[2 * e], s[2 * e + 1]), f2x, neg2), x0, x1);
+              const float p0 = ptx::ex2(x0), p1 = ptx::ex2(x1);
+              if (e & 1) acc1 = ptx::add_f32x2(acc1, ptx::f32x2(p0, p1));
+              else acc0 = ptx::add_f32x2(acc0, ptx::f32x2(p0, p1));
+              pk[e] = ptx::pack_f16x2(p0, p1);
+            }
           }
           float a0, a1, b0, b1;
           ptx::f32x2_split(acc0, a0, a1);
           ptx::f32x2_split(acc1, b0, b1);
           l += (a0 + b0) + (a1 + b1);
+          if constexpr (FEW) {  // the last P of these columns has been read
+            if (g >= 2 && !ptx::mbar_wait_warp(bar(C::B_PVDONE + b), ((g - 2) >> 1) & 1, abort_flag, a.timeout_ns,
+                                               kErrTimeout)) {
+              ok = false;
+              break;
+            }
+            ptx::tc_fence_after();
+          }
+          ptx::tmem_st16x2<N / 2>(lane_base + (b ? C::TM_P1 : C::TM_P0) + copy * (C::COLS / 2), pk);
           ptx::tmem_wait_st();
         }
         ptx::tc_fence_before();
@@ -811,122 +1057,7 @@ __global__ void __launch_bounds__(512, 1)
         if (lane == 0) ptx::mbar_arrive(bar(C::B_PFULL + b));
       }
       if (!ok) break;
-      have = run.next(a, &nextp);
-      // the next part's Q into TMEM now, so its S MMAs start during this epilogue
-      if (have && !copy_q(nextp)) {
-        ok = false;
-        break;
-      }
-      // ---- epilogue
-      if (!ptx::mbar_wait_warp(bar(C::B_PVDONE + ((g - 1) & 1)), ((g - 1) >> 1) & 1, abort_flag, a.timeout_ns,
-                               kErrTimeout)) {
-        ok = false;
-        break;
-      }
-      ptx::tc_fence_after();
-      const float lt = l + __shfl_xor_sync(0xffffffffu, l, 16);
-      const bool whole = part.cnt == part.nt;
-      const long grow0 = (static_cast<long>(part.n) * a.Hkv + part.hk) * a.R + part.rt * 128;
-      const long prow0 = static_cast<long>(2 * blockIdx.x + (part.t0 == 0 ? 1 : 0)) * a.part_rows;
-      // sums of my row over all copies
-      float M = m, L = lt;
-      if constexpr (K > 1) {
-        float2* ml = reinterpret_cast<float2*>(smem + C::OFF_J + C::J_BYTES);  // [copy][row]
-        constexpr int RB = 8 / K;  // row blocks
-        if (half == 0) ml[(copy * RB + rb) * 16 + (lane & 15)] = make_float2(m, lt);
-        if (!join()) {
-          ok = false;
-          break;
-        }
-        M = ninf;
-        L = 0.f;
-        if (warp_on) {
-#pragma unroll
-          for (int o = 0; o < K; ++o) M = fmaxf(M, ml[(o * RB + rb) * 16 + (lane & 15)].x);
-#pragma unroll
-          for (int o = 0; o < K; ++o) {
-            const float2 x = ml[(o * RB + rb) * 16 + (lane & 15)];
-            L += x.y == 0.f ? 0.f : x.y * ptx::ex2(x.x - M);
-          }
-        }
-      }
-      const bool empty = L == 0.f;
-      // a copy that saw no key left m at -inf and its O at zero
-      const float share = K == 1 || m == M ? 1.f : (m == ninf ? 0.f : ptx::ex2(m - M));
-      const float f = (empty ? 0.f : share / L) * pow2i(vref);
-      if (row_valid && half == 0 && copy == 0) {
-        const float lse2 = empty ? ninf : M - kPShift + ptx::lg2(L);
-        if (whole) a.lse[grow0 + r] = lse2 * 0.69314718055994530942f;
-        else a.l_part[prow0 + r] = lse2;
-      }
-#pragma unroll
-      for (int c = 0; c < D / 64; ++c) {
-        float v[32];
-        if (warp_on) {
-          uint32_t raw[32];
-          ptx::tmem_ld16x2_32<D / 2>(lane_base + C::TM_O + c * 32, raw);
-          ptx::tmem_wait_ld();
-          ptx::reg_fence32(raw);
-#pragma unroll
-          for (int e = 0; e < 32; ++e) v[e] = f == 0.f ? 0.f : __uint_as_float(raw[e]) * f;
-        }
-        if constexpr (K == 1) {
-          if (row_valid) {
-            uint4* o_dst = reinterpret_cast<uint4*>(a.o + (grow0 + r) * D) + half * (D / 16) + c * 4;
-            float4* p_dst = reinterpret_cast<float4*>(a.o_part + (prow0 + r) * D) + half * (D / 8) + c * 8;
-            if (whole) {
-#pragma unroll
-              for (int u = 0; u < 4; ++u)
-                o_dst[u] = make_uint4(ptx::pack_bf16x2(v[8 * u], v[8 * u + 1]), ptx::pack_bf16x2(v[8 * u + 2], v[8 * u + 3]),
-                                      ptx::pack_bf16x2(v[8 * u + 4], v[8 * u + 5]), ptx::pack_bf16x2(v[8 * u + 6], v[8 * u + 7]));
-            } else {
-#pragma unroll
-              for (int u = 0; u < 8; ++u) p_dst[u] = make_float4(v[4 * u], v[4 * u + 1], v[4 * u + 2], v[4 * u + 3]);
-            }
-          }
-        } else {
-          // [copy][row][16 float4], the float4 of a row permuted by the row
-          constexpr int RB = 8 / K;
-          float4* jb = reinterpret_cast<float4*>(smem + C::OFF_J);
-          if (c > 0 && !join()) {  // the previous columns have been read
-            ok = false;
-            break;
-          }
-          if (warp_on) {
-            float4* dst = jb + ((copy * RB + rb) * 16 + (lane & 15)) * 16;
-#pragma unroll
-            for (int u = 0; u < 8; ++u)
-              dst[(half * 8 + u) ^ (lane & 15)] = make_float4(v[4 * u], v[4 * u + 1], v[4 * u + 2], v[4 * u + 3]);
-          }
-          if (!join()) {
-            ok = false;
-            break;
-          }
-          const int tid = threadIdx.x;  // 0..255
-          for (int x = tid; x < rows * 16; x += 256) {
-            const int row = x >> 4, u = x & 15;
-            float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-            for (int o = 0; o < K; ++o) {
-              const float4 y = jb[(o * RB * 16 + row) * 16 + (u ^ (row & 15))];
-              sum.x += y.x;
-              sum.y += y.y;
-              sum.z += y.z;
-              sum.w += y.w;
-            }
-            // element: half u/8 of the row, 32 columns of this pass
-            const int e = (u >> 3) * (D / 2) + c * 32 + (u & 7) * 4;
-            if (whole)
-              *reinterpret_cast<uint2*>(a.o + (grow0 + row) * D + e) =
-                  make_uint2(ptx::pack_bf16x2(sum.x, sum.y), ptx::pack_bf16x2(sum.z, sum.w));
-            else
-              *reinterpret_cast<float4*>(a.o_part + (prow0 + row) * D + e) = sum;
-          }
-        }
-      }
-      if (!ok) break;
-      // the next part's first PV overwrites O only after this warp's next PFULL
-      // arrival, which follows the loads above
+      g = g_part + part.cnt;
     }
   }
 
@@ -962,7 +1093,7 @@ __global__ void __launch_bounds__(kCacheMaxCtas) cache_merge_kernel(const __grid
   const int r1 = min(min(128, a.R - rt * 128), r0 + kMergeRows);
   if (r0 >= r1) return;
   const long grow0 = (static_cast<long>(n) * a.Hkv + hk) * a.R + rt * 128;
-  const int nt = cache_tiles(cache_len(a, n));
+  const int nt = cache_tiles(a, cache_len(a, n));
   if (nt == 0) {
     ptx::grid_dep_wait();  // O and LSE may still be read by what ran before the attention kernel
     for (int r = r0 + warp; r < r1; r += WARPS) {
@@ -990,14 +1121,23 @@ __global__ void __launch_bounds__(kCacheMaxCtas) cache_merge_kernel(const __grid
   if (holds) s_slot[at + __popc(vote & ((1u << lane) - 1u))] = 2 * c + (b0 <= x0 ? 1 : 0);
   __syncthreads();
   ptx::grid_dep_wait();
+  using Vec = typename std::conditional<V == 4, float4, float2>::type;
+  constexpr int BATCH = 8;  // slots whose loads are in flight together
+  const long slot_stride = static_cast<long>(a.part_rows) * D;
   for (int r = r0 + warp; r < r1; r += WARPS) {
+    const float* base_o = a.o_part + static_cast<long>(r) * D + lane * V;
     float L = ninf, l[WARPS];
 #pragma unroll
     for (int u = 0; u < WARPS; ++u) {
       const int i = u * 32 + lane;
       l[u] = i < count ? a.l_part[static_cast<long>(s_slot[i]) * a.part_rows + r] : ninf;
-      L = fmaxf(L, l[u]);
     }
+    Vec x[BATCH];
+#pragma unroll
+    for (int u = 0; u < BATCH; ++u)
+      x[u] = *reinterpret_cast<const Vec*>(base_o + s_slot[min(u, count - 1)] * slot_stride);
+#pragma unroll
+    for (int u = 0; u < WARPS; ++u) L = fmaxf(L, l[u]);
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1) L = fmaxf(L, __shfl_xor_sync(0xffffffffu, L, off));
     const float base = L == ninf ? 0.f : L;
@@ -1007,13 +1147,21 @@ __global__ void __launch_bounds__(kCacheMaxCtas) cache_merge_kernel(const __grid
     float sum = 0.f, acc[V];
 #pragma unroll
     for (int e = 0; e < V; ++e) acc[e] = 0.f;
-#pragma unroll 8
-    for (int i = 0; i < count; ++i) {
-      const float w = s_w[warp][i];
-      const float* src = a.o_part + (static_cast<long>(s_slot[i]) * a.part_rows + r) * D + lane * V;
-      sum += w;
+#pragma unroll 1
+    for (int i = 0; i < count; i += BATCH) {
 #pragma unroll
-      for (int e = 0; e < V; ++e) acc[e] += w * src[e];
+      for (int u = 0; u < BATCH; ++u) {
+        const float w = i + u < count ? s_w[warp][i + u] : 0.f;
+        const float* y = reinterpret_cast<const float*>(&x[u]);
+        sum += w;
+#pragma unroll
+        for (int e = 0; e < V; ++e) acc[e] += i + u < count ? w * y[e] : 0.f;
+      }
+      if (i + BATCH < count) {
+#pragma unroll
+        for (int u = 0; u < BATCH; ++u)
+          x[u] = *reinterpret_cast<const Vec*>(base_o + s_slot[min(i + BATCH + u, count - 1)] * slot_stride);
+      }
     }
     __syncwarp();
     const float inv = sum == 0.f ? 0.f : 1.0f / sum;

@@ -90,24 +90,34 @@ __device__ __forceinline__ uint64_t cap_poly(uint64_t s, const uint64_t (&c)[5])
   return ptx::fma_f32x2(p, w, c[0]);
 }
 
-// s[0..N): bias of N consecutive keys from c0 on added, in log2 units; the
-// keys of a warp's tile are all left of its rows (side -1), all right (+1) or
-// around them (0).
+// s[0..N) = s * mul - slope2 * |at - c| for the N consecutive keys c from c0 on,
+// in log2 units. Distances are exact in fp32 up to 2^24; |at - c| is linear in
+// the key where a warp's keys all lie on one side of each thread's row: then
+// eight keys share a base and four pairs of offsets, two packed operations for
+// two scores.
 template <int N>
-__device__ __forceinline__ void add_bias(float (&s)[N], float slope2, int at, int c0, int side) {
-  // |at - c| with c = c0 + e: exact in fp32 up to 2^24
+__device__ __forceinline__ void scale_and_bias(float (&s)[N], float mul, float slope2, int at, int c0) {
   const float d0 = static_cast<float>(at - c0);
-  if (side == 0) {
+  if (__any_sync(0xffffffffu, at > c0 && at < c0 + N - 1)) {
 #pragma unroll
-    for (int e = 0; e < N; ++e) s[e] = fmaf(-slope2, fabsf(d0 - static_cast<float>(e)), s[e]);
+    for (int e = 0; e < N; ++e) s[e] = fmaf(-slope2, fabsf(d0 - static_cast<float>(e)), s[e] * mul);
   } else {
-    const float b1 = side < 0 ? slope2 : -slope2;  // per key
-    const float b0 = -slope2 * fabsf(d0);
-    const uint64_t b11 = ptx::f32x2(b1, b1), b00 = ptx::f32x2(b0, b0);
+    const float b1 = at > c0 ? slope2 : -slope2;  // per key: keys left of the row come nearer
+    uint64_t off[4];
 #pragma unroll
-    for (int e = 0; e < N; e += 2) {
-      const uint64_t t = ptx::fma_f32x2(ptx::f32x2(static_cast<float>(e), static_cast<float>(e + 1)), b11, b00);
-      ptx::f32x2_split(ptx::add_f32x2(ptx::f32x2(s[e], s[e + 1]), t), s[e], s[e + 1]);
+    for (int u = 0; u < 4; ++u) off[u] = ptx::f32x2(b1 * (2 * u), b1 * (2 * u + 1));
+    const uint64_t mul2 = ptx::f32x2(mul, mul);
+    const float b0 = -slope2 * fabsf(d0);
+#pragma unroll
+    for (int q = 0; q < N / 8; ++q) {
+      const float base = fmaf(b1, static_cast<float>(8 * q), b0);
+      const uint64_t base2 = ptx::f32x2(base, base);
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const int e = 8 * q + 2 * u;
+        ptx::f32x2_split(ptx::fma_f32x2(ptx::f32x2(s[e], s[e + 1]), mul2, ptx::add_f32x2(base2, off[u])), s[e],
+                         s[e + 1]);
+      }
     }
   }
 }
@@ -595,15 +605,10 @@ __global__ void __launch_bounds__(384, 1)
               ptx::f32x2_split(mul_f32x2(v, cap_poly(v, cap)), s[c], s[c + 1]);
             }
           }
-        } else if constexpr (BIAS) {
-          raw_args = false;
-#pragma unroll
-          for (int c = 0; c < BK; c += 2)
-            ptx::f32x2_split(mul_f32x2(ptx::f32x2(s[c], s[c + 1]), scale2), s[c], s[c + 1]);
         }
         if constexpr (BIAS) {
-          const int at0 = at - lane;  // the warp's first row
-          add_bias(s, slope2, at, c0, c0 + BK - 1 <= at0 ? -1 : (c0 >= at0 + 31 ? 1 : 0));
+          raw_args = false;
+          scale_and_bias(s, CAP ? 1.f : a.scale_log2, slope2, at, c0);
         }
         if (masked) {
 #pragma unroll

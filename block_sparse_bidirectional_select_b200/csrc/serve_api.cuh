@@ -7,6 +7,47 @@ namespace {
 inline bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 inline bool aligned2(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 1u) == 0; }
 
+// What the launches need of the current device, looked up once per device
+// (kernel attributes are per device too). Each entry is written whole before
+// `ready` is set; two threads that race write the same values.
+constexpr int kMaxDevices = 64;
+struct DeviceInfo {
+  std::atomic<int> ready{0};
+  int sms = 0;
+};
+DeviceInfo g_device_info[kMaxDevices];
+
+// The current device, which must be sm_100, and its SM count.
+int current_device(int* dev, int* sms) {
+  cudaError_t e = cudaGetDevice(dev);
+  if (e == cudaSuccess && *dev < kMaxDevices && g_device_info[*dev].ready.load(std::memory_order_acquire)) {
+    *sms = g_device_info[*dev].sms;
+    return SPARSED_OK;
+  }
+  SP_TRY(require_sm100());
+  SP_TRY(sm_count(sms));
+  if (*dev < kMaxDevices) {
+    g_device_info[*dev].sms = *sms;
+    g_device_info[*dev].ready.store(1, std::memory_order_release);
+  }
+  return SPARSED_OK;
+}
+
+// Raises a kernel's dynamic shared memory limit on the current device and
+// checks that its launch funds its register split (as launch_attn_t), once per
+// device and kernel (`done`: one bit per device, a static of the launcher).
+template <typename Kern>
+int prepare_kernel(Kern kern, int dev, int smem, int regs_needed, int threads, std::atomic<uint64_t>* done) {
+  const uint64_t bit = dev < kMaxDevices ? 1ull << dev : 0;
+  if (done->load(std::memory_order_acquire) & bit) return SPARSED_OK;
+  cudaFuncAttributes fa;
+  SP_CUDA(cudaFuncGetAttributes(&fa, kern));
+  if (fa.numRegs * threads < regs_needed) return SPARSED_ERR_UNSUPPORTED;
+  SP_CUDA(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem));
+  done->fetch_or(bit, std::memory_order_release);
+  return SPARSED_OK;
+}
+
 // fraction of 2^64 of x turns (x >= 0; whole turns dropped)
 uint64_t turn_fraction(double x) {
   x -= std::floor(x);
@@ -68,27 +109,24 @@ struct ScoredMaps {
 };
 
 template <int D, bool CAP, bool BIAS>
-int launch_scored_t(const ScoredMaps& t, const ScoredArgs& a, int grid, cudaStream_t st) {
+int launch_scored_t(const ScoredMaps& t, const ScoredArgs& a, int dev, int grid, cudaStream_t st) {
   using C = AttnCfg<D, 128>;
   auto kern = scored_attn_kernel<D, CAP, BIAS>;
-  // the register split must be funded by the launch (as launch_attn_t)
-  static int regs = -1;
-  if (regs < 0) {
-    cudaFuncAttributes fa;
-    SP_CUDA(cudaFuncGetAttributes(&fa, kern));
-    regs = fa.numRegs;
-  }
-  if (regs * C::THREADS < C::REGS_SOFTMAX * 256 + C::REGS_OTHER * (C::THREADS - 256)) return SPARSED_ERR_UNSUPPORTED;
-  SP_CUDA(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, ScoredCfg<D>::SMEM_BYTES));
+  static std::atomic<uint64_t> done{0};
+  SP_TRY(prepare_kernel(kern, dev, ScoredCfg<D>::SMEM_BYTES,
+                        C::REGS_SOFTMAX * 256 + C::REGS_OTHER * (C::THREADS - 256), C::THREADS, &done));
   kern<<<grid, C::THREADS, ScoredCfg<D>::SMEM_BYTES, st>>>(t.q, t.k, t.v, a);
   SP_CUDA(cudaGetLastError());
   return SPARSED_OK;
 }
 
 template <int D>
-int launch_scored(const ScoredMaps& t, const ScoredArgs& a, bool cap, int grid, cudaStream_t st) {
-  if (cap) return a.slopes ? launch_scored_t<D, true, true>(t, a, grid, st) : launch_scored_t<D, true, false>(t, a, grid, st);
-  return a.slopes ? launch_scored_t<D, false, true>(t, a, grid, st) : launch_scored_t<D, false, false>(t, a, grid, st);
+int launch_scored(const ScoredMaps& t, const ScoredArgs& a, bool cap, int dev, int grid, cudaStream_t st) {
+  if (cap)
+    return a.slopes ? launch_scored_t<D, true, true>(t, a, dev, grid, st)
+                    : launch_scored_t<D, true, false>(t, a, dev, grid, st);
+  return a.slopes ? launch_scored_t<D, false, true>(t, a, dev, grid, st)
+                  : launch_scored_t<D, false, false>(t, a, dev, grid, st);
 }
 
 // Capped scores in log2 units: y = s * P(s^2) while |s| * scale / cap <= 0.6,
@@ -124,10 +162,10 @@ CachePartLayout cache_part_layout(int B, int group, int d) {
 }
 
 // e4m3 [H, C, d] as a 3-D tensor map, boxes of whole rows.
-int make_map_cache(CUtensorMap* m, const uint8_t* ptr, long H, int C, int d, CUtensorMapSwizzle swizzle) {
+int make_map_cache(CUtensorMap* m, const uint8_t* ptr, long H, int C, int d, int rows, CUtensorMapSwizzle swizzle) {
   cuuint64_t dims[3] = {static_cast<cuuint64_t>(d), static_cast<cuuint64_t>(C), static_cast<cuuint64_t>(H)};
   cuuint64_t strides[2] = {static_cast<cuuint64_t>(d), static_cast<cuuint64_t>(C) * d};
-  cuuint32_t box[3] = {static_cast<cuuint32_t>(d), kCacheTile, 1};
+  cuuint32_t box[3] = {static_cast<cuuint32_t>(d), static_cast<cuuint32_t>(rows), 1};
   cuuint32_t es[3] = {1, 1, 1};
   CUresult r = g_encode(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<uint8_t*>(ptr), dims, strides, box, es,
                         CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
@@ -136,34 +174,36 @@ int make_map_cache(CUtensorMap* m, const uint8_t* ptr, long H, int C, int d, CUt
   return SPARSED_OK;
 }
 
-template <int D, bool MOD, int K>
-int launch_cache_attn(const uint8_t* k8, const uint8_t* v8, const CacheArgs& a, cudaStream_t st) {
-  using C = CacheCfg<D>;
+template <int D, bool MOD, int Q>
+int launch_cache_attn(const uint8_t* k8, const uint8_t* v8, CacheArgs& a, int dev, int sms, cudaStream_t st) {
+  using C = CacheCfg<D, Q>;
+  a.tile = C::BK;
   const unsigned items = static_cast<unsigned>(a.Hkv) * static_cast<unsigned>(a.RT);
-  int sms = 0;
-  SP_TRY(sm_count(&sms));
   if (sms > kCacheMaxCtas) sms = kCacheMaxCtas;
   // no more runs than there can be key tiles
-  const long most = static_cast<long>(a.N) * items * cdiv(a.C, kCacheTile);
+  const long most = static_cast<long>(a.N) * items * cdiv(a.C, C::BK);
+  if (most / sms >= (1l << 30)) return SPARSED_ERR_UNSUPPORTED;
   const int runs = static_cast<int>(most < sms ? most : sms);
   if (runs > 0) {
-    auto kern = cache_attn_kernel<D, MOD, K>;
-    // the register split must be funded by the launch (as launch_attn_t)
-    static int regs = -1;
-    if (regs < 0) {
-      cudaFuncAttributes fa;
-      SP_CUDA(cudaFuncGetAttributes(&fa, kern));
-      regs = fa.numRegs;
-    }
-    if (regs * C::THREADS < C::REGS_SOFTMAX * 256 + C::REGS_CONTROL * 128 + C::REGS_WIDEN * 128)
-      return SPARSED_ERR_UNSUPPORTED;
+    auto kern = cache_attn_kernel<D, MOD, Q>;
+    static std::atomic<uint64_t> done{0};
+    SP_TRY(prepare_kernel(kern, dev, C::SMEM_BYTES,
+                          C::REGS_TOTAL, C::THREADS, &done));
     CUtensorMap tk, tv;
     const long H = static_cast<long>(a.N) * a.Hkv;
-    SP_TRY(make_map_cache(&tk, k8, H, a.C, D, D == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B));
-    SP_TRY(make_map_cache(&tv, v8, H, a.C, D, CU_TENSOR_MAP_SWIZZLE_NONE));
-    SP_CUDA(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM_BYTES));
+    SP_TRY(make_map_cache(&tk, k8, H, a.C, D, C::BK, D == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B));
+    SP_TRY(make_map_cache(&tv, v8, H, a.C, D, C::BK, CU_TENSOR_MAP_SWIZZLE_NONE));
     kern<<<runs, C::THREADS, C::SMEM_BYTES, st>>>(tk, tv, a);
     SP_CUDA(cudaGetLastError());
+  }
+  // The merge kernel asks for the attention kernel's split of an SM's memory:
+  // its CTAs can then sit beside the last runs, and no SM changes its split.
+  static std::atomic<uint64_t> merge_done{0};
+  const uint64_t bit = dev < kMaxDevices ? 1ull << dev : 0;
+  if (!(merge_done.load(std::memory_order_acquire) & bit)) {
+    SP_CUDA(cudaFuncSetAttribute(cache_merge_kernel<D>, cudaFuncAttributePreferredSharedMemoryCarveout,
+                                 cudaSharedmemCarveoutMaxShared));
+    merge_done.fetch_or(bit, std::memory_order_release);
   }
   const unsigned row_groups = static_cast<unsigned>(cdiv(a.R < 128 ? a.R : 128, kMergeRows));
   return launch_k(cache_merge_kernel<D>, dim3(items, static_cast<unsigned>(a.N), row_groups), dim3(kCacheMaxCtas), 0,
@@ -189,7 +229,8 @@ int sparsed_rope_axes(const uint16_t* X, size_t x_stride_h, size_t x_stride_l, c
   if (J > kRopeMaxPairs) return SPARSED_ERR_UNSUPPORTED;
   if (H == 0 || L == 0) return SPARSED_OK;
   if (!X || !Y || !positions || !aligned2(X) || !aligned2(Y) || !aligned4(positions)) return SPARSED_ERR_INVALID_ARG;
-  SP_TRY(require_sm100());
+  int dev = 0, sms = 0;
+  SP_TRY(current_device(&dev, &sms));
   RopeArgs a;
   a.x = X;
   a.y = Y;
@@ -203,14 +244,33 @@ int sparsed_rope_axes(const uint16_t* X, size_t x_stride_h, size_t x_stride_l, c
   a.d = d;
   a.J = static_cast<int>(J);
   a.sign = inverse ? -1 : 1;
-  int j = 0;
-  for (int s = 0; s < n_axes; ++s)
-    for (int i = 0; i < sections[s]; ++i, ++j) {
-      const double ex = shared_ladder ? static_cast<double>(j) / static_cast<double>(J)
-                                      : static_cast<double>(i) / sections[s];
-      a.turn[j] = turn_fraction(std::pow(static_cast<double>(theta), -ex) * 0.15915494309189533577);
-      a.axis[j] = static_cast<uint8_t>(s);
-    }
+  // the ladder of frequencies, kept from the thread's last call with the same
+  // axes (J powers cost more than the launch)
+  struct Ladder {
+    float theta = 0.f;
+    int shared = -1, n_axes = 0, sections[kRopeMaxAxes];
+    uint64_t turn[kRopeMaxPairs];
+    uint8_t axis[kRopeMaxPairs];
+  };
+  static thread_local Ladder ladder;
+  const int shared = shared_ladder != 0;
+  if (ladder.theta != theta || ladder.shared != shared || ladder.n_axes != n_axes ||
+      std::memcmp(ladder.sections, sections, n_axes * sizeof(int)) != 0) {
+    ladder.theta = theta;
+    ladder.shared = shared;
+    ladder.n_axes = n_axes;
+    std::memcpy(ladder.sections, sections, n_axes * sizeof(int));
+    int j = 0;
+    for (int s = 0; s < n_axes; ++s)
+      for (int i = 0; i < sections[s]; ++i, ++j) {
+        const double ex = shared ? static_cast<double>(j) / static_cast<double>(J)
+                                 : static_cast<double>(i) / sections[s];
+        ladder.turn[j] = turn_fraction(std::pow(static_cast<double>(theta), -ex) * 0.15915494309189533577);
+        ladder.axis[j] = static_cast<uint8_t>(s);
+      }
+  }
+  std::memcpy(a.turn, ladder.turn, J * sizeof(uint64_t));
+  std::memcpy(a.axis, ladder.axis, J);
   a.rot_units = static_cast<int>(cdiv(J, 8));
   a.units = a.rot_units + static_cast<int>(cdiv(d - 2 * J, 8));
   const bool vec = J % 8 == 0 && aligned16(X) && aligned16(Y) &&
@@ -218,8 +278,6 @@ int sparsed_rope_axes(const uint16_t* X, size_t x_stride_h, size_t x_stride_l, c
   const long gx = cdiv(L, kRopeThreads / a.units);
   // as many heads per CTA as leave about four CTAs per SM: a CTA takes its
   // sines and cosines once for all its heads
-  int sms = 0;
-  SP_TRY(sm_count(&sms));
   long share = gx * H / (4l * sms);
   share = share < 1 ? 1 : (share > 16 ? 16 : share);
   a.heads_per_cta = static_cast<int>(share < H ? share : H);
@@ -244,7 +302,8 @@ int sparsed_cache_append(const uint16_t* K, size_t k_stride_n, size_t k_stride_h
   if (!aligned2(K) || !aligned2(V) || !aligned16(k8) || !aligned16(v8) || !aligned4(k_scale) || !aligned4(v_scale) ||
       !aligned4(start) || !aligned4(count))
     return SPARSED_ERR_INVALID_ARG;
-  SP_TRY(require_sm100());
+  int dev = 0, sms = 0;
+  SP_TRY(current_device(&dev, &sms));
   AppendArgs a;
   a.x[0] = K;
   a.x[1] = V;
@@ -299,7 +358,8 @@ int sparsed_cache_attn(const uint16_t* Q, size_t q_stride_n, size_t q_stride_h, 
   if (((q_stride_n | q_stride_h | q_stride_b) & 7u) != 0) return SPARSED_ERR_INVALID_ARG;
   const CachePartLayout w = cache_part_layout(B, Hq / Hkv, d);
   if (!workspace || workspace_bytes < w.total || (reinterpret_cast<uintptr_t>(workspace) & 255u)) return SPARSED_ERR_WORKSPACE;
-  SP_TRY(require_sm100());
+  int dev = 0, sms = 0;
+  SP_TRY(current_device(&dev, &sms));
   SP_TRY(get_encoder());
   CacheArgs a = {};
   a.q = Q;
@@ -334,22 +394,19 @@ int sparsed_cache_attn(const uint16_t* Q, size_t q_stride_n, size_t q_stride_h, 
   if (items >= (1l << 31)) return SPARSED_ERR_UNSUPPORTED;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   const bool mod = a.capped || a.slopes;
-  // as many copies of the rows as the accumulators' 128 lanes hold
-  const int copies = R <= 32 ? 4 : (R <= 64 ? 2 : 1);
-#define SP_CACHE(D_, MOD_, K_) \
-  if (d == D_ && mod == MOD_ && copies == K_) return launch_cache_attn<D_, MOD_, K_>(k8, v8, a, st);
-  SP_CACHE(64, false, 1)
-  SP_CACHE(64, false, 2)
-  SP_CACHE(64, false, 4)
-  SP_CACHE(64, true, 1)
-  SP_CACHE(64, true, 2)
-  SP_CACHE(64, true, 4)
-  SP_CACHE(128, false, 1)
-  SP_CACHE(128, false, 2)
-  SP_CACHE(128, false, 4)
-  SP_CACHE(128, true, 1)
-  SP_CACHE(128, true, 2)
-  SP_CACHE(128, true, 4)
+  // the few-rows form as far as its lanes reach, with the most copies of the rows
+  const int form = R <= 16 ? 4 : (R <= 32 ? 2 : (R <= 64 ? 1 : 0));
+#define SP_CACHE(D_, MOD_)                                                                       \
+  if (d == D_ && mod == MOD_) {                                                                  \
+    if (form == 4) return launch_cache_attn<D_, MOD_, 4>(k8, v8, a, dev, sms, st);               \
+    if (form == 2) return launch_cache_attn<D_, MOD_, 2>(k8, v8, a, dev, sms, st);               \
+    if (form == 1) return launch_cache_attn<D_, MOD_, 1>(k8, v8, a, dev, sms, st);               \
+    return launch_cache_attn<D_, MOD_, 0>(k8, v8, a, dev, sms, st);                              \
+  }
+  SP_CACHE(64, false)
+  SP_CACHE(64, true)
+  SP_CACHE(128, false)
+  SP_CACHE(128, true)
 #undef SP_CACHE
   return SPARSED_ERR_UNSUPPORTED;
 }
@@ -360,7 +417,8 @@ int sparsed_document_ranges(const int32_t* starts, const int32_t* prefix, int n_
   if (L == 0) return SPARSED_OK;
   if (!starts || !ranges || !aligned4(starts) || !aligned4(prefix) || (reinterpret_cast<uintptr_t>(ranges) & 7u))
     return SPARSED_ERR_INVALID_ARG;
-  SP_TRY(require_sm100());
+  int dev = 0, sms = 0;
+  SP_TRY(current_device(&dev, &sms));
   document_ranges_kernel<<<static_cast<unsigned>(cdiv(L, 256)), 256, 0, static_cast<cudaStream_t>(stream)>>>(
       starts, prefix, n_docs, L, reinterpret_cast<int2*>(ranges));
   SP_CUDA(cudaGetLastError());
@@ -396,7 +454,8 @@ int sparsed_scored_attn(const uint16_t* Q, size_t q_stride_h, size_t q_stride_l,
   size_t need = 0;
   SP_TRY(sparsed_scored_attn_workspace_bytes(Hq, Lq, &need));
   if (!workspace || workspace_bytes < need || (reinterpret_cast<uintptr_t>(workspace) & 255u)) return SPARSED_ERR_WORKSPACE;
-  SP_TRY(require_sm100());
+  int dev = 0, sms = 0;
+  SP_TRY(current_device(&dev, &sms));
   SP_TRY(get_encoder());
   ScoredMaps t;
   SP_TRY(make_map_strided(&t.q, Q, Hq, Lq, d, q_stride_h, q_stride_l, 128));
@@ -406,8 +465,6 @@ int sparsed_scored_attn(const uint16_t* Q, size_t q_stride_h, size_t q_stride_l,
   } else {
     t.k = t.v = t.q;  // no key, no tile is read
   }
-  int sms = 0;
-  SP_TRY(sm_count(&sms));
   ScoredArgs a = {};
   a.H = Hq;
   a.group = Hq / Hkv;
@@ -434,7 +491,7 @@ int sparsed_scored_attn(const uint16_t* Q, size_t q_stride_h, size_t q_stride_l,
     SP_CUDA(cudaMemsetAsync(a.sched, 0, sizeof(int), st));
   }
   const int grid = static_cast<int>(turns < sms ? turns : sms);
-  return d == 64 ? launch_scored<64>(t, a, softcap > 0.f, grid, st) : launch_scored<128>(t, a, softcap > 0.f, grid, st);
+  return d == 64 ? launch_scored<64>(t, a, softcap > 0.f, dev, grid, st) : launch_scored<128>(t, a, softcap > 0.f, dev, grid, st);
 }
 
 }  // extern "C"

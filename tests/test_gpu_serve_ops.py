@@ -196,6 +196,11 @@ def check_cache_attn(q, c, lengths, softcap=0.0, slopes=None, q_start=None, scal
     (2, 6, 2, 61, 448, [100, 448]),          # 183 rows of a kv head: two row tiles, the last ragged
     (1, 2, 1, 64, 16384, [16001]),
     (1, 1, 1, 300, 192, [130]),
+    (2, 2, 2, 48, 1024, [1000, 65]),         # 48 rows
+    (3, 3, 1, 8, 704, [704, 8, 641]),        # 24 rows
+    (5, 15, 1, 1, 2048, [2048, 1, 0, 2047, 64]),
+    (40, 2, 2, 1, 128, [1 + (37 * n) % 128 for n in range(40)]),   # several items to a run
+    (33, 1, 1, 20, 64, [20 + n for n in range(33)]),
 ])
 def test_cache_attn(d, N, Hq, Hkv, B, C, lengths):
     g = gen(N + Hq * 10 + B)
@@ -211,6 +216,8 @@ def test_cache_attn_modified_scores(softcap, bias, given):
     q = randn(g, 2, 8, 5, 128, scale=4.0)     # scores that reach the cap
     slopes = torch.tensor([2.0 ** -(h + 1) for h in range(8)], device="cuda") if bias else None
     check_cache_attn(q, c, [1088, 700], softcap, slopes, [3, 2000] if given else None)
+    check_cache_attn(randn(g, 2, 8, 61, 128, scale=4.0), c, [1088, 700], softcap, slopes, [500, -90] if given else None)
+    check_cache_attn(randn(g, 2, 8, 9, 128, scale=4.0), c, [70, 1001], softcap, None if slopes is None else slopes * 30)
 
 
 def test_cache_attn_far_scales_and_large_queries():
