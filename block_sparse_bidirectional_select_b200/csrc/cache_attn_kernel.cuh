@@ -80,7 +80,6 @@ struct CacheArgs {
   const float* slopes;             // or null
   float cap_c[5];                  // as ScoredArgs
   float cap_fast, cap_in, cap_log2;
-  int capped;
   uint16_t* o;                     // [N, Hkv * group, B, D]
   float* lse;
   float* o_part;                   // [2 * CTAs][part_rows][D]
@@ -96,23 +95,24 @@ struct CacheCfg {
   static constexpr int N = COLS / 2;             // ... for one thread
   static constexpr int T8 = BK * D;              // bytes of an e4m3 tile
   static constexpr int T16 = 2 * T8;
-  static constexpr int KS = D == 64 ? 8 : (FEW ? 6 : 4);  // ring stages of K and of V
+  static constexpr int VT = FEW ? 2 : 1;         // tiles of a V stage, widened together
+  static constexpr int KS = D == 64 ? 8 : (FEW ? 6 : 4);  // ring stages of K
+  static constexpr int VS = KS / VT;                      // ... of V
   static constexpr int ROWS = FEW ? 64 / Q : 128;        // rows of a row tile at most
   static constexpr int OFF_K = 0;
   static constexpr int OFF_V = OFF_K + KS * T8;
-  static constexpr int WS = FEW ? 4 : 2;         // buffers of widened V
-  static constexpr int OFF_W = OFF_V + KS * T8;
-  static constexpr int OFF_J = OFF_W + WS * T16;  // joining copies: 128 lanes x 64 fp32, then (m, l) of each lane
+  static constexpr int OFF_W = OFF_V + VS * VT * T8;  // widened V: two buffers of VT tiles
+  static constexpr int OFF_J = OFF_W + 2 * VT * T16;  // joining copies: 128 lanes x 64 fp32, then (m, l) of each lane
   static constexpr int J_BYTES = FEW ? 128 * 64 * 4 : 0;
   static constexpr int OFF_Q = OFF_J + J_BYTES + (FEW ? 128 * 8 : 0);  // a part's Q: hi, lo, exponents
   static constexpr int OFF_BAR = OFF_Q + 2 * ROWS * D + ROWS * 4;
   static constexpr int B_KFULL = 0;
   static constexpr int B_KEMPTY = B_KFULL + KS;
   static constexpr int B_VFULL = B_KEMPTY + KS;
-  static constexpr int B_VEMPTY = B_VFULL + KS;  // 4 converter-warp arrivals
-  static constexpr int B_WFULL = B_VEMPTY + KS;  // [WS] 4 converter-warp arrivals
-  static constexpr int B_WEMPTY = B_WFULL + WS;  // [WS]
-  static constexpr int B_SFULL = B_WEMPTY + WS;  // [2]
+  static constexpr int B_VEMPTY = B_VFULL + VS;  // 4 converter-warp arrivals
+  static constexpr int B_WFULL = B_VEMPTY + VS;  // [2] 4 converter-warp arrivals
+  static constexpr int B_WEMPTY = B_WFULL + 2;   // [2]
+  static constexpr int B_SFULL = B_WEMPTY + 2;   // [2]
   static constexpr int B_SREAD = B_SFULL + 2;    // [2] FEW: S read, its owners' 4 warp arrivals
   static constexpr int B_PFULL = B_SREAD + 2;    // [2] its owners' warp arrivals
   static constexpr int B_PVDONE = B_PFULL + 2;   // [2]
@@ -142,14 +142,11 @@ struct CacheCfg {
   // K rows of D bytes: one swizzle span of 128 or 64 bytes, 8 rows a group
   static constexpr uint32_t HI_K = ((8u * D) >> 4) | (1u << 14) | ((D == 128 ? 2u : 4u) << 29);
   static constexpr int THREADS = 512;
-  // Few rows leave 8192 registers and some shared memory of an SM to the merge
-  // kernel, whose CTAs then wait in place while the last runs end.
-  static constexpr int REGS_LAUNCH = FEW ? 112 : 128;
-  static constexpr int REGS_SOFTMAX = FEW ? 152 : 184, REGS_CONTROL = 56, REGS_WIDEN = FEW ? 80 : 88;
+  static constexpr int REGS_SOFTMAX = 184, REGS_CONTROL = 56, REGS_WIDEN = 88;
   static constexpr int REGS_TOTAL = 256 * REGS_SOFTMAX + 128 * REGS_CONTROL + 128 * REGS_WIDEN;
   static_assert(TM_Q1 + D / 2 <= 512, "TMEM budget");
-  static_assert(SMEM_BYTES <= (FEW ? 225280 : 232448), "shared memory budget");
-  static_assert(REGS_TOTAL <= REGS_LAUNCH * THREADS, "register budget");
+  static_assert(SMEM_BYTES <= 232448, "shared memory budget");
+  static_assert(REGS_TOTAL <= 65536, "register budget");
 };
 
 namespace ptx {
@@ -345,8 +342,9 @@ __device__ __forceinline__ void load_scores(uint32_t taddr, float (&s)[N]) {
   }
 }
 
-template <int D, bool MOD, int Q>
-__global__ void __launch_bounds__(CacheCfg<D, Q>::THREADS) __maxnreg__((CacheCfg<D, Q>::REGS_LAUNCH))
+// MODE: 0 plain scores, 1 with a distance bias, 2 capped (and biased, if slopes are given).
+template <int D, int MODE, int Q>
+__global__ void __launch_bounds__(CacheCfg<D, Q>::THREADS, 1)
     cache_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                       const __grid_constant__ CacheArgs a) {
   using C = CacheCfg<D, Q>;
@@ -365,18 +363,18 @@ __global__ void __launch_bounds__(CacheCfg<D, Q>::THREADS) __maxnreg__((CacheCfg
 
   // ---- setup
   if (threadIdx.x == 0) {
-    for (int s = 0; s < C::WS; ++s) {
-      ptx::mbar_init(bar(C::B_WFULL + s), 4);
-      ptx::mbar_init(bar(C::B_WEMPTY + s), 1);
-    }
     for (int s = 0; s < C::KS; ++s) {
       ptx::mbar_init(bar(C::B_KFULL + s), 1);
       ptx::mbar_init(bar(C::B_KEMPTY + s), 1);
+    }
+    for (int s = 0; s < C::VS; ++s) {
       ptx::mbar_init(bar(C::B_VFULL + s), 1);
       ptx::mbar_init(bar(C::B_VEMPTY + s), 4);
     }
     for (int b = 0; b < 2; ++b) {
         ptx::mbar_init(bar(C::B_SREAD + b), C::OWNERS);
+      ptx::mbar_init(bar(C::B_WFULL + b), 4);
+      ptx::mbar_init(bar(C::B_WEMPTY + b), 1);
       ptx::mbar_init(bar(C::B_SFULL + b), 1);
       ptx::mbar_init(bar(C::B_PFULL + b), C::OWNERS);
       ptx::mbar_init(bar(C::B_PVDONE + b), 1);
@@ -460,7 +458,8 @@ __global__ void __launch_bounds__(CacheCfg<D, Q>::THREADS) __maxnreg__((CacheCfg
     const int tid = threadIdx.x - 384;
     constexpr int TPR = D / 16;            // threads of a row, 16 values each
     constexpr int ROWS = 128 / TPR;        // rows of a pass
-    constexpr int NP = C::BK / ROWS;
+    constexpr int NP = C::BK / ROWS;       // passes of a tile
+    constexpr int PER = C::BK / kCacheBlock;  // scale blocks of a tile
     const int j = tid % TPR, row0 = tid / TPR;
     const int chunk = j >> 2;
     // The two 16-byte units of a thread's f16 values. With 128 elements a row,
@@ -470,41 +469,45 @@ __global__ void __launch_bounds__(CacheCfg<D, Q>::THREADS) __maxnreg__((CacheCfg
     const int swz = row0 & 7;  // ROWS is a multiple of 8
     const uint32_t off_a = row0 * 128 + (((2 * (j & 3) + (sw ? 1 : 0)) ^ swz) << 4) + chunk * (C::BK * 128);
     const uint32_t off_b = row0 * 128 + (((2 * (j & 3) + (sw ? 0 : 1)) ^ swz) << 4) + chunk * (C::BK * 128);
-    int g = 0;
+    int pp = 0;  // V stages so far (VT tiles each, fewer at a part's end)
     bool ok = true;
     while (ok && run.next(a, part)) {
       const int vref = part_vref(a, part, lane);
       const float* vs = a.v_scale + (static_cast<long>(part.n) * a.Hkv + part.hk) * (a.C / kCacheBlock);
       const int last = a.C / kCacheBlock - 1;
-      constexpr int PER = C::BK / kCacheBlock;  // scale blocks of a tile
-      // a tile's scales are read a tile ahead
+      // a stage's scales are read a stage ahead
+      constexpr int SB = C::VT * PER;  // scale blocks of a stage: tile t - x / PER, block x % PER
       const int t_last = part.t0 + part.cnt - 1;
-      float sc[PER];
+      auto scale_at = [&](int t, int x) -> float {
+        return vs[min(max(PER * (t - x / PER) + x % PER, 0), last)];
+      };
+      float sc[SB];
 #pragma unroll
-      for (int x = 0; x < PER; ++x) sc[x] = vs[min(PER * t_last + x, last)];
-      for (int t = t_last; t >= part.t0; --t, ++g) {
-        const int st = g % C::KS, ws = g % C::WS;
-        const int valid = part.len - t * C::BK;
+      for (int x = 0; x < SB; ++x) sc[x] = scale_at(t_last, x);
+#pragma unroll 1
+      for (int t = t_last; t >= part.t0; t -= C::VT, ++pp) {
+        const int st = pp % C::VS, b = pp & 1;
         // 2^(ev - vref) as f16 pairs (0 below f16's range; a block past the
         // length may hold any scale: its rows are cleared)
-        uint32_t mul[PER];
+        uint32_t mul[SB];
 #pragma unroll
-        for (int x = 0; x < PER; ++x) {
+        for (int x = 0; x < SB; ++x) {
           const int dlt = min(scale_exponent(sc[x]) - vref, 0);
           const uint32_t hbits = dlt >= -14 ? static_cast<uint32_t>(dlt + 15) << 10
                                             : (dlt >= -24 ? 1u << (dlt + 24) : 0u);
           mul[x] = hbits | (hbits << 16);
-          if (t > part.t0) sc[x] = vs[PER * (t - 1) + x];
+          sc[x] = scale_at(t - C::VT, x);
         }
-        if (!ptx::mbar_wait_warp(bar(C::B_VFULL + st), (g / C::KS) & 1, abort_flag, a.timeout_ns, kErrTimeout)) {
+        if (!ptx::mbar_wait_warp(bar(C::B_VFULL + st), (pp / C::VS) & 1, abort_flag, a.timeout_ns, kErrTimeout)) {
           ok = false;
           break;
         }
-        const uint8_t* src = smem + C::OFF_V + st * C::T8 + row0 * D + j * 16;
-        uint8_t* dst = smem + C::OFF_W + ws * C::T16;
-        uint4 x[NP];
+        const uint8_t* src = smem + C::OFF_V + st * (C::VT * C::T8) + row0 * D + j * 16;
+        uint8_t* dst = smem + C::OFF_W + b * (C::VT * C::T16);
+        const int valid = part.len - t * C::BK;  // of the stage's first tile; a second one is whole
+        uint4 x[C::VT * NP];
 #pragma unroll
-        for (int p = 0; p < NP; ++p) x[p] = *reinterpret_cast<const uint4*>(src + p * (ROWS * D));
+        for (int p = 0; p < C::VT * NP; ++p) x[p] = *reinterpret_cast<const uint4*>(src + p * (ROWS * D));
         __syncwarp();
         if (lane == 0) ptx::mbar_arrive(bar(C::B_VEMPTY + st));
         if (valid < C::BK) {
@@ -512,13 +515,13 @@ __global__ void __launch_bounds__(CacheCfg<D, Q>::THREADS) __maxnreg__((CacheCfg
           for (int p = 0; p < NP; ++p)
             if (row0 + p * ROWS >= valid) x[p] = make_uint4(0, 0, 0, 0);
         }
-        if (g >= C::WS &&
-            !ptx::mbar_wait_warp(bar(C::B_WEMPTY + ws), (g / C::WS - 1) & 1, abort_flag, a.timeout_ns, kErrTimeout)) {
+        if (pp >= 2 &&
+            !ptx::mbar_wait_warp(bar(C::B_WEMPTY + b), ((pp >> 1) - 1) & 1, abort_flag, a.timeout_ns, kErrTimeout)) {
           ok = false;
           break;
         }
 #pragma unroll
-        for (int p = 0; p < NP; ++p) {
+        for (int p = 0; p < C::VT * NP; ++p) {
           const uint32_t m2 = mul[p * PER / NP];
           const uint32_t w[4] = {sw ? x[p].z : x[p].x, sw ? x[p].w : x[p].y, sw ? x[p].x : x[p].z, sw ? x[p].y : x[p].w};
           uint32_t h[8];
@@ -531,12 +534,13 @@ __global__ void __launch_bounds__(CacheCfg<D, Q>::THREADS) __maxnreg__((CacheCfg
             asm("mul.rn.f16x2 %0, %0, %1;" : "+r"(h[2 * e]) : "r"(m2));
             asm("mul.rn.f16x2 %0, %0, %1;" : "+r"(h[2 * e + 1]) : "r"(m2));
           }
-          *reinterpret_cast<uint4*>(dst + off_a + p * (ROWS * 128)) = make_uint4(h[0], h[1], h[2], h[3]);
-          *reinterpret_cast<uint4*>(dst + off_b + p * (ROWS * 128)) = make_uint4(h[4], h[5], h[6], h[7]);
+          uint8_t* tile = dst + (p / NP) * C::T16 + (p % NP) * (ROWS * 128);
+          *reinterpret_cast<uint4*>(tile + off_a) = make_uint4(h[0], h[1], h[2], h[3]);
+          *reinterpret_cast<uint4*>(tile + off_b) = make_uint4(h[4], h[5], h[6], h[7]);
         }
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         __syncwarp();
-        if (lane == 0) ptx::mbar_arrive(bar(C::B_WFULL + ws));
+        if (lane == 0) ptx::mbar_arrive(bar(C::B_WFULL + b));
       }
     }
   } else if (warp >= 8) {
@@ -551,11 +555,12 @@ __global__ void __launch_bounds__(CacheCfg<D, Q>::THREADS) __maxnreg__((CacheCfg
         ptx::tma_prefetch_desc(&tm_k);
         ptx::tma_prefetch_desc(&tm_v);
       }
-      int g = 0, issued_k = 0, issued_v = 0;
+      int g = 0, pp = 0;  // K tiles, V stages issued
       bool ok = true;
       while (ok && run.next(a, part)) {
         const int z = part.n * a.Hkv + part.hk;
-        for (int t = part.t0 + part.cnt - 1; t >= part.t0; --t, ++g) {
+        for (int jj = 0; jj < part.cnt; ++jj, ++g) {
+          const int t = part.t0 + part.cnt - 1 - jj;
           const int st = g % C::KS;
           if (g >= C::KS && !wait(C::B_KEMPTY + st, g / C::KS - 1)) {
             ok = false;
@@ -563,24 +568,30 @@ __global__ void __launch_bounds__(CacheCfg<D, Q>::THREADS) __maxnreg__((CacheCfg
           }
           ptx::mbar_arrive_expect_tx_if(leader, bar(C::B_KFULL + st), C::T8);
           ptx::tma_load_3d_if(leader, sb + C::OFF_K + st * C::T8, &tm_k, bar(C::B_KFULL + st), 0, t * C::BK, z);
-          issued_k = g + 1;
-          if (g >= C::KS && !wait(C::B_VEMPTY + st, g / C::KS - 1)) {
+          if (jj % C::VT != 0) continue;
+          // the V stage that begins with this tile
+          const int sv = pp % C::VS;
+          if (pp >= C::VS && !wait(C::B_VEMPTY + sv, pp / C::VS - 1)) {
+            ++g;
             ok = false;
             break;
           }
-          ptx::mbar_arrive_expect_tx_if(leader, bar(C::B_VFULL + st), C::T8);
-          ptx::tma_load_3d_if(leader, sb + C::OFF_V + st * C::T8, &tm_v, bar(C::B_VFULL + st), 0, t * C::BK, z);
-          issued_v = g + 1;
+          const int tiles = min(C::VT, part.cnt - jj);
+          ptx::mbar_arrive_expect_tx_if(leader, bar(C::B_VFULL + sv), tiles * C::T8);
+          for (int x = 0; x < tiles; ++x)
+            ptx::tma_load_3d_if(leader, sb + C::OFF_V + (sv * C::VT + x) * C::T8, &tm_v, bar(C::B_VFULL + sv), 0,
+                                (t - x) * C::BK, z);
+          ++pp;
         }
       }
       if (!ok) {
         // let the copies in flight land before the CTA's shared memory goes away
         const uint64_t short_ns = a.timeout_ns / 4;
         volatile int dummy = 0;
-        for (int u = (issued_k > C::KS ? issued_k - C::KS : 0); u < issued_k; ++u)
+        for (int u = (g > C::KS ? g - C::KS : 0); u < g; ++u)
           ptx::mbar_wait(bar(C::B_KFULL + u % C::KS), (u / C::KS) & 1, &dummy, short_ns, 0);
-        for (int u = (issued_v > C::KS ? issued_v - C::KS : 0); u < issued_v; ++u)
-          ptx::mbar_wait(bar(C::B_VFULL + u % C::KS), (u / C::KS) & 1, &dummy, short_ns, 0);
+        for (int u = (pp > C::VS ? pp - C::VS : 0); u < pp; ++u)
+          ptx::mbar_wait(bar(C::B_VFULL + u % C::VS), (u / C::VS) & 1, &dummy, short_ns, 0);
         __syncwarp();
       }
     } else if (warp == 9) {
@@ -629,24 +640,27 @@ __global__ void __launch_bounds__(CacheCfg<D, Q>::THREADS) __maxnreg__((CacheCfg
       // ============================================================ PV issuer
       constexpr uint32_t HI = ptx::sdesc_sw128_hi(1024);
       const uint32_t vlo = ptx::sdesc_sw128_lo(sb + C::OFF_W, C::BK * 128);
-      int g = 0;
+      int g = 0, pp = 0;
       bool ok = true;
       while (ok && run.next(a, part)) {
         for (int t = 0; t < part.cnt; ++t, ++g) {
-          const int b = g & 1, ws = g % C::WS;
-          if (!wait(C::B_WFULL + ws, g / C::WS) || !wait(C::B_PFULL + b, g >> 1)) {
+          const int b = g & 1, x = t % C::VT, wb = pp & 1;
+          if ((x == 0 && !wait(C::B_WFULL + wb, pp >> 1)) || !wait(C::B_PFULL + b, g >> 1)) {
             ok = false;
             break;
           }
           ptx::tc_fence_after();
-          const uint32_t b0 = vlo + static_cast<uint32_t>(ws * C::T16 >> 4);
+          const uint32_t b0 = vlo + static_cast<uint32_t>((wb * C::VT + x) * C::T16 >> 4);
           const uint32_t p_tmem = tmem + (b ? C::TM_P1 : C::TM_P0);
 #pragma unroll
           for (int kk = 0; kk < C::BK / 16; ++kk)
             ptx::umma_ts_lohi_if(leader, tmem + C::TM_O, p_tmem + kk * 8, b0 + kk * (2048 >> 4), HI, C::IDESC_PV,
                                  (t > 0 || kk > 0) ? 1u : 0u);
           ptx::umma_commit_if(leader, bar(C::B_PVDONE + b));
-          ptx::umma_commit_if(leader, bar(C::B_WEMPTY + ws));
+          if (x == C::VT - 1 || t == part.cnt - 1) {
+            ptx::umma_commit_if(leader, bar(C::B_WEMPTY + wb));
+            ++pp;
+          }
         }
       }
       if (!ok) {
@@ -671,7 +685,7 @@ __global__ void __launch_bounds__(CacheCfg<D, Q>::THREADS) __maxnreg__((CacheCfg
     const uint32_t lane_base = tmem + (static_cast<uint32_t>(quad * 32 + hw * 16) << 16);
     const float ninf = -__int_as_float(0x7f800000);
     uint64_t cap[5];
-    if constexpr (MOD) {
+    if constexpr (MODE == 2) {
 #pragma unroll
       for (int u = 0; u < 5; ++u) cap[u] = ptx::f32x2(a.cap_c[u], a.cap_c[u]);
     }
@@ -912,7 +926,7 @@ __global__ void __launch_bounds__(CacheCfg<D, Q>::THREADS) __maxnreg__((CacheCfg
       const float qmul = pow2i(eq_new);
       float slope2 = 0.f;
       int at = 0;
-      if constexpr (MOD) {
+      if constexpr (MODE != 0) {
         const int rr = min(part.rt * 128 + r, a.R - 1);
         const int hg = rr / a.B;
         if (a.slopes) slope2 = a.slopes[part.hk * a.group + hg] * 1.44269504088896340736f;
@@ -952,39 +966,37 @@ __global__ void __launch_bounds__(CacheCfg<D, Q>::THREADS) __maxnreg__((CacheCfg
         }
         if (warp_on) {
           float f = fminf(f2 * a.scale_log2, 1e37f);
+          // keys past the length, in an item's last tile only
           const int valid = part.len - t * C::BK - key0;
-          if constexpr (MOD) {
-            f = 1.f;
-            if (valid < N) {  // what lies past the length has no say in the path taken
+          const bool ragged = t == part.nt - 1;
+          if constexpr (MODE == 2) {
+            if (ragged) {  // ... have no say in the path taken
 #pragma unroll
               for (int c = 0; c < N; ++c)
                 if (c >= valid) s[c] = 0.f;
             }
-            if (a.capped) {
-              const uint64_t f22 = ptx::f32x2(f2, f2);
+            const uint64_t f22 = ptx::f32x2(f2, f2);
 #pragma unroll
-              for (int c = 0; c < N; c += 2)
-                ptx::f32x2_split(mul_f32x2(ptx::f32x2(s[c], s[c + 1]), f22), s[c], s[c + 1]);
-              const bool wide = __any_sync(0xffffffffu, fmaxf(row_max(s), -row_min(s)) > a.cap_fast);
-              if (wide) {
+            for (int c = 0; c < N; c += 2)
+              ptx::f32x2_split(mul_f32x2(ptx::f32x2(s[c], s[c + 1]), f22), s[c], s[c + 1]);
+            if (__any_sync(0xffffffffu, fmaxf(row_max(s), -row_min(s)) > a.cap_fast)) {
 #pragma unroll
-                for (int c = 0; c < N; ++c) s[c] = a.cap_log2 * tanh_wide(s[c] * a.cap_in);
-              } else {
+              for (int c = 0; c < N; ++c) s[c] = a.cap_log2 * tanh_wide(s[c] * a.cap_in);
+            } else {
 #pragma unroll
-                for (int c = 0; c < N; c += 2) {
-                  const uint64_t v = ptx::f32x2(s[c], s[c + 1]);
-                  ptx::f32x2_split(mul_f32x2(v, cap_poly(v, cap)), s[c], s[c + 1]);
-                }
+              for (int c = 0; c < N; c += 2) {
+                const uint64_t v = ptx::f32x2(s[c], s[c + 1]);
+                ptx::f32x2_split(mul_f32x2(v, cap_poly(v, cap)), s[c], s[c + 1]);
               }
             }
-            const float ff = a.capped ? 1.f : fminf(f2 * a.scale_log2, 1e37f);
-            if (a.slopes) {
-              scale_and_bias(s, ff, slope2, at, t * C::BK + key0);
-            } else if (!a.capped) {
-              f = ff;
-            }
+            f = 1.f;
+            if (a.slopes) scale_and_bias(s, 1.f, slope2, at, t * C::BK + key0);
           }
-          if (valid < N) {
+          if constexpr (MODE == 1) {
+            scale_and_bias(s, f, slope2, at, t * C::BK + key0);
+            f = 1.f;
+          }
+          if (ragged) {
 #pragma unroll
             for (int c = 0; c < N; ++c)
               if (c >= valid) s[c] = ninf;
@@ -1023,7 +1035,7 @@ __global__ void __launch_bounds__(CacheCfg<D, Q>::THREADS) __maxnreg__((CacheCfg
           uint64_t acc0 = ptx::f32x2(0.f, 0.f), acc1 = acc0;
           uint32_t pk[N / 2];
           // with a steep bias whole tiles lie where 2^x is exactly 0
-          if (MOD && !__any_sync(0xffffffffu, !(mx + neg < -127.f))) {
+          if (MODE != 0 && !__any_sync(0xffffffffu, !(mx + neg < -127.f))) {
 #pragma unroll
             for (int e = 0; e < N / 2; ++e) pk[e] = 0u;
           } else {

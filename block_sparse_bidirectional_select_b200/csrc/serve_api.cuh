@@ -174,7 +174,7 @@ int make_map_cache(CUtensorMap* m, const uint8_t* ptr, long H, int C, int d, int
   return SPARSED_OK;
 }
 
-template <int D, bool MOD, int Q>
+template <int D, int MODE, int Q>
 int launch_cache_attn(const uint8_t* k8, const uint8_t* v8, CacheArgs& a, int dev, int sms, cudaStream_t st) {
   using C = CacheCfg<D, Q>;
   a.tile = C::BK;
@@ -185,7 +185,7 @@ int launch_cache_attn(const uint8_t* k8, const uint8_t* v8, CacheArgs& a, int de
   if (most / sms >= (1l << 30)) return SPARSED_ERR_UNSUPPORTED;
   const int runs = static_cast<int>(most < sms ? most : sms);
   if (runs > 0) {
-    auto kern = cache_attn_kernel<D, MOD, Q>;
+    auto kern = cache_attn_kernel<D, MODE, Q>;
     static std::atomic<uint64_t> done{0};
     SP_TRY(prepare_kernel(kern, dev, C::SMEM_BYTES,
                           C::REGS_TOTAL, C::THREADS, &done));
@@ -383,8 +383,8 @@ int sparsed_cache_attn(const uint16_t* Q, size_t q_stride_n, size_t q_stride_h, 
   a.scale_log2 = scale * 1.44269504088896340736f;
   if (a.scale_log2 < 1.17549435e-38f) a.scale_log2 = 1.17549435e-38f;  // as scored_attn
   a.slopes = slopes;
-  a.capped = softcap > 0.f;
-  if (a.capped) cap_coefficients(scale, softcap, a.cap_c, &a.cap_fast, &a.cap_in, &a.cap_log2);
+  const int mode = softcap > 0.f ? 2 : (slopes ? 1 : 0);
+  if (mode == 2) cap_coefficients(scale, softcap, a.cap_c, &a.cap_fast, &a.cap_in, &a.cap_log2);
   a.o = O;
   a.lse = LSE;
   a.o_part = static_cast<float*>(workspace);
@@ -393,20 +393,21 @@ int sparsed_cache_attn(const uint16_t* Q, size_t q_stride_n, size_t q_stride_h, 
   const long items = static_cast<long>(Hkv) * a.RT;
   if (items >= (1l << 31)) return SPARSED_ERR_UNSUPPORTED;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  const bool mod = a.capped || a.slopes;
   // the few-rows form as far as its lanes reach, with the most copies of the rows
   const int form = R <= 16 ? 4 : (R <= 32 ? 2 : (R <= 64 ? 1 : 0));
-#define SP_CACHE(D_, MOD_)                                                                       \
-  if (d == D_ && mod == MOD_) {                                                                  \
-    if (form == 4) return launch_cache_attn<D_, MOD_, 4>(k8, v8, a, dev, sms, st);               \
-    if (form == 2) return launch_cache_attn<D_, MOD_, 2>(k8, v8, a, dev, sms, st);               \
-    if (form == 1) return launch_cache_attn<D_, MOD_, 1>(k8, v8, a, dev, sms, st);               \
-    return launch_cache_attn<D_, MOD_, 0>(k8, v8, a, dev, sms, st);                              \
+#define SP_CACHE(D_, MODE_)                                                                      \
+  if (d == D_ && mode == MODE_) {                                                                \
+    if (form == 4) return launch_cache_attn<D_, MODE_, 4>(k8, v8, a, dev, sms, st);              \
+    if (form == 2) return launch_cache_attn<D_, MODE_, 2>(k8, v8, a, dev, sms, st);              \
+    if (form == 1) return launch_cache_attn<D_, MODE_, 1>(k8, v8, a, dev, sms, st);              \
+    return launch_cache_attn<D_, MODE_, 0>(k8, v8, a, dev, sms, st);                             \
   }
-  SP_CACHE(64, false)
-  SP_CACHE(64, true)
-  SP_CACHE(128, false)
-  SP_CACHE(128, true)
+  SP_CACHE(64, 0)
+  SP_CACHE(64, 1)
+  SP_CACHE(64, 2)
+  SP_CACHE(128, 0)
+  SP_CACHE(128, 1)
+  SP_CACHE(128, 2)
 #undef SP_CACHE
   return SPARSED_ERR_UNSUPPORTED;
 }
