@@ -78,7 +78,7 @@ struct CacheArgs {
   int tile;                        // keys of a tile
   float scale_log2;                // above 0
   const float* slopes;             // or null
-  float cap_c[5];                  // as ScoredArgs
+  float cap_c[4];                  // as ScoredArgs
   float cap_fast, cap_in, cap_log2;
   uint16_t* o;                     // [N, Hkv * group, B, D]
   float* lse;
@@ -220,14 +220,6 @@ __device__ __forceinline__ void reg_fence8(uint32_t (&r)[8]) {
 __device__ __forceinline__ void reg_fence16(uint32_t (&r)[16]) {
   asm volatile("" : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
                "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]));
-}
-template <int R>
-__device__ __forceinline__ void setmaxnreg_inc() {
-  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(R) : "memory");
-}
-template <int R>
-__device__ __forceinline__ void setmaxnreg_dec() {
-  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(R) : "memory");
 }
 }  // namespace ptx
 
@@ -454,7 +446,7 @@ __global__ void __launch_bounds__(CacheCfg<D, Q>::THREADS, 1)
 
   if (warp >= 12) {
     // ================================================================ widen V
-    ptx::setmaxnreg_dec<C::REGS_WIDEN>();
+    setmaxnreg_dec<C::REGS_WIDEN>();
     const int tid = threadIdx.x - 384;
     constexpr int TPR = D / 16;            // threads of a row, 16 values each
     constexpr int ROWS = 128 / TPR;        // rows of a pass
@@ -544,7 +536,7 @@ __global__ void __launch_bounds__(CacheCfg<D, Q>::THREADS, 1)
       }
     }
   } else if (warp >= 8) {
-    ptx::setmaxnreg_dec<C::REGS_CONTROL>();
+    setmaxnreg_dec<C::REGS_CONTROL>();
     const uint32_t leader = ptx::elect_one();
     auto wait = [&](int idx, int parity) -> bool {
       return ptx::mbar_wait_warp(bar(idx), parity & 1, abort_flag, a.timeout_ns, kErrTimeout);
@@ -672,7 +664,7 @@ __global__ void __launch_bounds__(CacheCfg<D, Q>::THREADS, 1)
     }
   } else {
     // ================================================================ softmax
-    ptx::setmaxnreg_inc<C::REGS_SOFTMAX>();
+    setmaxnreg_inc<C::REGS_SOFTMAX>();
     const int half = lane >> 4;
     const int quad = warp & 3, hw = warp >> 2;
     // lanes 16*hw.. of quarter `quad` hold the 16 rows of block rb, for the
@@ -684,10 +676,10 @@ __global__ void __launch_bounds__(CacheCfg<D, Q>::THREADS, 1)
     const int sblk = key0 / kCacheBlock;           // ... its scale block in the tile
     const uint32_t lane_base = tmem + (static_cast<uint32_t>(quad * 32 + hw * 16) << 16);
     const float ninf = -__int_as_float(0x7f800000);
-    uint64_t cap[5];
+    uint64_t cap[4];
     if constexpr (MODE == 2) {
 #pragma unroll
-      for (int u = 0; u < 5; ++u) cap[u] = ptx::f32x2(a.cap_c[u], a.cap_c[u]);
+      for (int u = 0; u < 4; ++u) cap[u] = ptx::f32x2(a.cap_c[u], a.cap_c[u]);
     }
     int g = 0;
     int joins = 0;  // phases of B_JOIN

@@ -15,19 +15,23 @@
 //     that are not inside the ranges of all its 32 rows;
 //   * the scores are modified in registers between the TMEM load and the
 //     exponentials (below);
+//   * with a distance bias the tiles are walked from the pair's own position
+//     outwards, so that the row maxima are set at once (towards the position,
+//     every tile would raise them and rescale O), and a warp whose scores all
+//     lie where 2^x is exactly 0 stores zeros;
 //   * with ranges, warp 11 clears the V rows of a tile that no row of the pair
 //     sees, so that whatever padding holds (0 * NaN) stays out of O. It looks
 //     closer only at tiles that no single row sees whole;
 //   * when the pairs would leave SMs idle, a CTA takes single query tiles.
 //
-// Capped scores. tanh(u) = u * P(u^2) for |u| <= 0.6, P of degree 4 by a
-// minimax fit (absolute error 2e-8; the coefficients are scaled on the host so
-// that the polynomial takes the raw product and gives log2 units). It costs
-// six packed FP32 operations for two scores, two of which replace the scaling
-// of the plain path. A warp whose tile holds a larger score takes
-// 1 - 2 / (1 + e^2u), two MUFU operations, whose absolute error (2^-23) is as
-// good; MUFU is what bounds that path (16 operations a clock and SM, three
-// per score with the softmax's own).
+// Capped scores. tanh(u) = u * P(u^2) for |u| <= 0.5, P of degree 3 by a
+// minimax fit (absolute error 1.3e-7, the rounding of a score of that size; the
+// coefficients are scaled on the host so that the polynomial takes the raw
+// product and gives log2 units). It costs five packed FP32 operations for two
+// scores, one of which replaces the scaling of the plain path. A warp whose
+// tile holds a larger score takes 1 - 2 / (1 + e^2u), two MUFU operations,
+// whose absolute error (2^-23) is as good; MUFU is what bounds that path (16
+// operations a clock and SM, three per score with the softmax's own).
 #pragma once
 
 #include <type_traits>
@@ -46,7 +50,7 @@ struct ScoredArgs {
   const int2* ranges;       // [L] or null
   // capped scores: y = s * P(s^2) in log2 units while |s| <= cap_fast, else
   // cap_log2 * tanh(s * cap_in)
-  float cap_c[5];
+  float cap_c[4];
   float cap_fast, cap_in, cap_log2;
   float* lse;               // [H, L]
   uint16_t* o;              // [H, L, D]
@@ -62,10 +66,19 @@ struct ScoredCfg {
   static constexpr int B_VOK = A::NUM_BARS;           // [NST] V tile cleared of unseen rows
   static constexpr int NUM_BARS = B_VOK + NST;
   static constexpr int N_WTAKERS = A::N_WTAKERS + 1;  // and warp 11
-  static constexpr int OFF_MISC = A::OFF_BAR + NUM_BARS * 8;  // tmem slot, abort flag, 2 x (pair, first tile, tiles)
-  static constexpr int SMEM_BYTES = OFF_MISC + 32 + 1024;
+  static constexpr int OFF_MISC = A::OFF_BAR + NUM_BARS * 8;  // tmem slot, abort flag, 2 x (pair, first tile, tiles, near)
+  static constexpr int SMEM_BYTES = OFF_MISC + 48 + 1024;
   static_assert(SMEM_BYTES <= A::SMEM_LIMIT, "shared memory budget");
 };
+
+template <int R>
+__device__ __forceinline__ void setmaxnreg_inc() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(R) : "memory");
+}
+template <int R>
+__device__ __forceinline__ void setmaxnreg_dec() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(R) : "memory");
+}
 
 // tanh(u) for any u: 1 - 2 / (1 + 2^(2 u log2 e)); saturates to +-1.
 __device__ __forceinline__ float tanh_wide(float u) {
@@ -82,10 +95,9 @@ __device__ __forceinline__ uint64_t mul_f32x2(uint64_t a, uint64_t b) {
 }
 
 // P(s^2) for a pair of raw scores.
-__device__ __forceinline__ uint64_t cap_poly(uint64_t s, const uint64_t (&c)[5]) {
+__device__ __forceinline__ uint64_t cap_poly(uint64_t s, const uint64_t (&c)[4]) {
   const uint64_t w = mul_f32x2(s, s);
-  uint64_t p = ptx::fma_f32x2(c[4], w, c[3]);
-  p = ptx::fma_f32x2(p, w, c[2]);
+  uint64_t p = ptx::fma_f32x2(c[3], w, c[2]);
   p = ptx::fma_f32x2(p, w, c[1]);
   return ptx::fma_f32x2(p, w, c[0]);
 }
@@ -136,21 +148,31 @@ __device__ __forceinline__ float row_max(const float (&s)[N]) {
   }
   return fmaxf(fmaxf(mx0, mx1), fmaxf(mx2, mx3));
 }
+// Three-input minimum (one instruction).
+__device__ __forceinline__ float min3(float a, float b, float c) {
+  float d;
+  asm("min.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
 template <int N>
 __device__ __forceinline__ float row_min(const float (&s)[N]) {
-  float m0 = s[0], m1 = s[1];
+  float mn0 = s[0], mn1 = s[1], mn2 = s[2], mn3 = s[3];
 #pragma unroll
-  for (int c = 2; c < N; c += 2) {
-    m0 = fminf(m0, s[c]);
-    m1 = fminf(m1, s[c + 1]);
+  for (int c = 4; c < N; c += 8) {
+    mn0 = min3(mn0, s[c], s[c + 1]);
+    mn1 = min3(mn1, s[c + 2], s[c + 3]);
+    if (c + 4 < N) {
+      mn2 = min3(mn2, s[c + 4], s[c + 5]);
+      mn3 = min3(mn3, s[c + 6], s[c + 7]);
+    }
   }
-  return fminf(m0, m1);
+  return fminf(fminf(mn0, mn1), fminf(mn2, mn3));
 }
 
 // The exponentials of 32 scores of a row in log2 units: CAPPED takes raw
 // scores through the polynomial on the way.
 template <bool CAPPED>
-__device__ __forceinline__ void scored_exp32(const float* s, uint64_t mul2, uint64_t negm2, const uint64_t (&cap)[5],
+__device__ __forceinline__ void scored_exp32(const float* s, uint64_t mul2, uint64_t negm2, const uint64_t (&cap)[4],
                                              uint32_t (&pk)[16], uint64_t& acc0, uint64_t& acc1) {
 #pragma unroll
   for (int e = 0; e < 16; ++e) {
@@ -179,6 +201,9 @@ __device__ __forceinline__ ScoredPair scored_pair(const ScoredArgs& a, int w, in
   r.has1 = a.qpp == 2 && r.q0 + 1 < a.nqb;
   return r;
 }
+
+// The walk's j-th tile: from tile `near` down to the first, then on upwards.
+__device__ __forceinline__ int scored_tile(int j, int near) { return j <= near ? near - j : j; }
 
 // [lo, hi) of row r clamped to the keys; rows past the last see all of them
 // when `outside_all`, else nothing.
@@ -211,7 +236,8 @@ __global__ void __launch_bounds__(384, 1)
   const int n_pairs = a.H * nph;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + S::OFF_MISC);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + S::OFF_MISC + 4);
-  // the producer publishes each turn here, double-buffered: pair, first key tile, key tiles
+  // the producer publishes each turn here, double-buffered: pair, first key
+  // tile, key tiles, and the tile that the walk starts from (scored_tile)
   volatile int* turn = reinterpret_cast<volatile int*>(smem + S::OFF_MISC + 8);
   auto bar = [&](int idx) -> uint32_t { return sb + C::OFF_BAR + 8 * idx; };
 
@@ -286,13 +312,14 @@ __global__ void __launch_bounds__(384, 1)
         return true;
       };
       int np = 0;  // turns published
-      auto publish = [&](int w, int j0, int nj) -> bool {
+      auto publish = [&](int w, int j0, int nj, int near) -> bool {
         const int b = np & 1;
         if (np >= 2 && !wait(C::B_WEMPTY + b, (np >> 1) - 1)) return false;
         if (leader) {
-          turn[3 * b] = w;
-          turn[3 * b + 1] = j0;
-          turn[3 * b + 2] = nj;
+          turn[4 * b] = w;
+          turn[4 * b + 1] = j0;
+          turn[4 * b + 2] = nj;
+          turn[4 * b + 3] = near;
           ptx::mbar_arrive(bar(C::B_WFULL + b));
         }
         __syncwarp();
@@ -302,7 +329,7 @@ __global__ void __launch_bounds__(384, 1)
       int w = blockIdx.x;
       while (ok) {
         if (w >= n_pairs) {
-          publish(n_pairs, 0, 0);
+          publish(n_pairs, 0, 0, 0);
           break;
         }
         const ScoredPair pr = scored_pair(a, w, nph);
@@ -326,7 +353,10 @@ __global__ void __launch_bounds__(384, 1)
         }
         const int j0 = lo / BK;
         const int nj = hi > lo ? (hi + BK - 1) / BK - j0 : 0;
-        ok = publish(w, j0, nj);
+        // with a bias, the tile of the middle of the pair's rows
+        const int near =
+            BIAS ? min(max((a.q_start + pr.q0 * 128 + (pr.has1 ? 128 : 64)) / BK - j0, 0), max(nj - 1, 0)) : 0;
+        ok = publish(w, j0, nj, near);
         if (!ok) break;
         // the CTA's next turn: the static stride, or a claim on the counter
         int w_next = w + static_cast<int>(gridDim.x);
@@ -346,9 +376,10 @@ __global__ void __launch_bounds__(384, 1)
         // in the order the slots consume them: Q0, K_0, Q1, V_0, K_1, V_1, ...
         for (int j = 0; ok && j < nj; ++j) {
           if (j == 0) ok = load_q(0, pr.q0);
-          if (ok) ok = load_tile(&tm_k, j0 + j);
+          const int blk = j0 + (BIAS ? scored_tile(j, near) : j);
+          if (ok) ok = load_tile(&tm_k, blk);
           if (ok && pr.has1 && j == 0) ok = load_q(1, pr.q0 + 1);
-          if (ok) ok = load_tile(&tm_v, j0 + j);
+          if (ok) ok = load_tile(&tm_v, blk);
         }
         w = w_next;
       }
@@ -382,8 +413,8 @@ __global__ void __launch_bounds__(384, 1)
           ok = false;
           break;
         }
-        const int w = turn[3 * (np & 1)];
-        const int nj = turn[3 * (np & 1) + 2];
+        const int w = turn[4 * (np & 1)];
+        const int nj = turn[4 * (np & 1) + 2];
         __syncwarp();
         if (lane == 0) ptx::mbar_arrive(bar(C::B_WEMPTY + (np & 1)));
         if (w >= n_pairs) break;
@@ -455,7 +486,8 @@ __global__ void __launch_bounds__(384, 1)
       bool ok = true;
       for (int np = 0; ok; ++np) {
         if (!wait(C::B_WFULL + (np & 1), np >> 1)) break;
-        const int w = turn[3 * (np & 1)], j0 = turn[3 * (np & 1) + 1], nj = turn[3 * (np & 1) + 2];
+        const int w = turn[4 * (np & 1)], j0 = turn[4 * (np & 1) + 1], nj = turn[4 * (np & 1) + 2];
+        const int near = turn[4 * (np & 1) + 3];
         __syncwarp();
         if (lane == 0) ptx::mbar_arrive(bar(C::B_WEMPTY + (np & 1)));
         if (w >= n_pairs) break;
@@ -479,7 +511,7 @@ __global__ void __launch_bounds__(384, 1)
             ok = false;
             break;
           }
-          const int c0 = (j0 + j) * BK;
+          const int c0 = (j0 + (BIAS ? scored_tile(j, near) : j)) * BK;
           bool whole = false;
 #pragma unroll
           for (int u = 0; u < 8; ++u) whole |= rg[u].x <= c0 && rg[u].y >= c0 + BK;
@@ -529,10 +561,10 @@ __global__ void __launch_bounds__(384, 1)
     const float ninf = -__int_as_float(0x7f800000);
     const uint64_t scale2 = ptx::f32x2(a.scale_log2, a.scale_log2);
     const uint64_t one2 = ptx::f32x2(1.f, 1.f);
-    uint64_t cap[5];
+    uint64_t cap[4];
     if constexpr (CAP) {
 #pragma unroll
-      for (int u = 0; u < 5; ++u) cap[u] = ptx::f32x2(a.cap_c[u], a.cap_c[u]);
+      for (int u = 0; u < 4; ++u) cap[u] = ptx::f32x2(a.cap_c[u], a.cap_c[u]);
     }
     int tcount = 0;  // tiles of this slot so far (SFULL / PVDONE phases)
     bool ok = true;
@@ -541,7 +573,8 @@ __global__ void __launch_bounds__(384, 1)
         ok = false;
         break;
       }
-      const int w = turn[3 * (np & 1)], j0 = turn[3 * (np & 1) + 1], nj = turn[3 * (np & 1) + 2];
+      const int w = turn[4 * (np & 1)], j0 = turn[4 * (np & 1) + 1], nj = turn[4 * (np & 1) + 2];
+      const int near = turn[4 * (np & 1) + 3];
       __syncwarp();
       if (lane == 0) ptx::mbar_arrive(bar(C::B_WEMPTY + (np & 1)));
       if (w >= n_pairs) break;
@@ -562,7 +595,7 @@ __global__ void __launch_bounds__(384, 1)
       float m = ninf;  // running row max, log2 units
       float l = 0.f;   // running row sum
       for (int jj = 0; jj < nj; ++jj, ++tcount) {
-        const int c0 = (j0 + jj) * BK;
+        const int c0 = (j0 + (BIAS ? scored_tile(jj, near) : jj)) * BK;
         if (!ptx::mbar_wait_warp(bar(C::B_SFULL + slot), tcount & 1, abort_flag, a.timeout_ns, kErrTimeout)) {
           ok = false;
           break;
@@ -645,11 +678,18 @@ __global__ void __launch_bounds__(384, 1)
         const uint64_t negm2 = ptx::f32x2(-mu, -mu);
         uint64_t acc0 = ptx::f32x2(0.f, 0.f), acc1 = acc0;
         constexpr int CPP = BK / 32 / C::NPV;  // 32-column chunks per part of P
+        // with a steep bias whole tiles lie where 2^x is exactly 0
+        const bool zero = BIAS && !__any_sync(0xffffffffu, !(mx - mu < -127.f));
         auto exp_pass = [&](auto capped, uint64_t mul2) {
 #pragma unroll
           for (int c = 0; c < BK / 32; ++c) {
             uint32_t pk[16];
-            scored_exp32<decltype(capped)::value>(s + 32 * c, mul2, negm2, cap, pk, acc0, acc1);
+            if (zero) {
+#pragma unroll
+              for (int e = 0; e < 16; ++e) pk[e] = 0u;
+            } else {
+              scored_exp32<decltype(capped)::value>(s + 32 * c, mul2, negm2, cap, pk, acc0, acc1);
+            }
             ptx::tmem_st32_16(lane_base + s_col + c * 16, pk);
             if ((c + 1) % CPP == 0 && c + 1 < BK / 32) {
               // this part of P is in TMEM: its PV MMAs may start

@@ -129,22 +129,21 @@ int launch_scored(const ScoredMaps& t, const ScoredArgs& a, bool cap, int dev, i
                   : launch_scored_t<D, false, false>(t, a, dev, grid, st);
 }
 
-// Capped scores in log2 units: y = s * P(s^2) while |s| * scale / cap <= 0.6,
-// with tanh(u) = u * (c0 + c1 u^2 + ... + c4 u^8) to 2e-8 there (minimax fit).
-void cap_coefficients(float scale, float softcap, float (&c)[5], float* fast, float* in, float* cap_log2) {
-  constexpr double kC[5] = {0.9999996274072432, -0.3333120858238067, 0.13299210120915597, -0.051696738736441226,
-                            0.014976954257328949};
+// Capped scores in log2 units: y = s * P(s^2) while |s| * scale / cap <= 0.5,
+// with tanh(u) = u * (c0 + c1 u^2 + c2 u^4 + c3 u^6) to 1.3e-7 there (minimax fit).
+void cap_coefficients(float scale, float softcap, float (&c)[4], float* fast, float* in, float* cap_log2) {
+  constexpr double kC[4] = {0.9999976761831301, -0.3332065518031203, 0.1314514529551474, -0.04337247410609953};
   const double u = static_cast<double>(scale) / softcap, cl = softcap * 1.4426950408889634;
   double f = cl * u;
   bool finite = true;
-  for (int i = 0; i < 5; ++i, f *= u * u) {
+  for (int i = 0; i < 4; ++i, f *= u * u) {
     c[i] = static_cast<float>(kC[i] * f);
     finite = finite && std::isfinite(c[i]);
   }
   *in = static_cast<float>(u);
   *cap_log2 = static_cast<float>(cl);
   // above this the wide form; everywhere if the polynomial does not fit fp32
-  *fast = !finite ? -1.f : (u > 0 && 0.6 / u < 1e18 ? static_cast<float>(0.6 / u) : 1e18f);
+  *fast = !finite ? -1.f : (u > 0 && 0.5 / u < 1e18 ? static_cast<float>(0.5 / u) : 1e18f);
 }
 
 // Partial results of cache_attn: two slots per CTA.
