@@ -24,14 +24,16 @@
 //     closer only at tiles that no single row sees whole;
 //   * when the pairs would leave SMs idle, a CTA takes single query tiles.
 //
-// Capped scores. tanh(u) = u * P(u^2) for |u| <= 0.5, P of degree 3 by a
-// minimax fit (absolute error 1.3e-7, the rounding of a score of that size; the
-// coefficients are scaled on the host so that the polynomial takes the raw
-// product and gives log2 units). It costs five packed FP32 operations for two
-// scores, one of which replaces the scaling of the plain path. A warp whose
-// tile holds a larger score takes 1 - 2 / (1 + e^2u), two MUFU operations,
-// whose absolute error (2^-23) is as good; MUFU is what bounds that path (16
-// operations a clock and SM, three per score with the softmax's own).
+// Capped scores. tanh(u) = u * P(u^2), P by a minimax fit (the coefficients are
+// scaled on the host so that the polynomial takes the raw product and gives
+// log2 units): of degree 2 for |u| <= 0.25 (absolute error 5e-8) and 3 for
+// |u| <= 0.5 (1.3e-7, the rounding of a score of that size). The narrow one
+// costs four packed FP32 operations for two scores, one of which replaces the
+// scaling of the plain path; a packed operation takes the FP32 pipe two clocks,
+// which is what a capped pass pays for. A warp whose tile holds a larger score
+// takes 1 - 2 / (1 + e^2u), two MUFU operations, whose absolute error (2^-23) is
+// as good; MUFU is what bounds that path (16 operations a clock and SM, three
+// per score with the softmax's own).
 #pragma once
 
 #include <type_traits>
@@ -48,9 +50,9 @@ struct ScoredArgs {
   const float* slopes;      // [H] or null
   int q_start;
   const int2* ranges;       // [L] or null
-  // capped scores: y = s * P(s^2) in log2 units while |s| <= cap_fast, else
-  // cap_log2 * tanh(s * cap_in)
-  float cap_c[4];
+  // capped scores: y = s * P(s^2) in log2 units while |s| <= cap_fast, with a
+  // narrow P (cap_n) up to half of it, else cap_log2 * tanh(s * cap_in)
+  float cap_c[4], cap_n[3];
   float cap_fast, cap_in, cap_log2;
   float* lse;               // [H, L]
   uint16_t* o;              // [H, L, D]
@@ -94,7 +96,11 @@ __device__ __forceinline__ uint64_t mul_f32x2(uint64_t a, uint64_t b) {
   return d;
 }
 
-// P(s^2) for a pair of raw scores.
+// P(s^2) for a pair of raw scores; the narrow one has a term less.
+__device__ __forceinline__ uint64_t cap_poly_narrow(uint64_t s, const uint64_t (&c)[3]) {
+  const uint64_t w = mul_f32x2(s, s);
+  return ptx::fma_f32x2(ptx::fma_f32x2(c[2], w, c[1]), w, c[0]);
+}
 __device__ __forceinline__ uint64_t cap_poly(uint64_t s, const uint64_t (&c)[4]) {
   const uint64_t w = mul_f32x2(s, s);
   uint64_t p = ptx::fma_f32x2(c[3], w, c[2]);
@@ -170,15 +176,17 @@ __device__ __forceinline__ float row_min(const float (&s)[N]) {
 }
 
 // The exponentials of 32 scores of a row in log2 units: CAPPED takes raw
-// scores through the polynomial on the way.
-template <bool CAPPED>
+// scores through a polynomial on the way (1: the narrow one).
+template <int CAPPED>
 __device__ __forceinline__ void scored_exp32(const float* s, uint64_t mul2, uint64_t negm2, const uint64_t (&cap)[4],
+                                             const uint64_t (&cap_n)[3],
                                              uint32_t (&pk)[16], uint64_t& acc0, uint64_t& acc1) {
 #pragma unroll
   for (int e = 0; e < 16; ++e) {
     const uint64_t v = ptx::f32x2(s[2 * e], s[2 * e + 1]);
     uint64_t arg;
-    if constexpr (CAPPED) arg = ptx::fma_f32x2(v, cap_poly(v, cap), negm2);
+    if constexpr (CAPPED == 2) arg = ptx::fma_f32x2(v, cap_poly(v, cap), negm2);
+    else if constexpr (CAPPED == 1) arg = ptx::fma_f32x2(v, cap_poly_narrow(v, cap_n), negm2);
     else arg = ptx::fma_f32x2(v, mul2, negm2);
     float x0, x1;
     ptx::f32x2_split(arg, x0, x1);
@@ -561,10 +569,12 @@ __global__ void __launch_bounds__(384, 1)
     const float ninf = -__int_as_float(0x7f800000);
     const uint64_t scale2 = ptx::f32x2(a.scale_log2, a.scale_log2);
     const uint64_t one2 = ptx::f32x2(1.f, 1.f);
-    uint64_t cap[4];
+    uint64_t cap[4], cap_n[3];
     if constexpr (CAP) {
 #pragma unroll
       for (int u = 0; u < 4; ++u) cap[u] = ptx::f32x2(a.cap_c[u], a.cap_c[u]);
+#pragma unroll
+      for (int u = 0; u < 3; ++u) cap_n[u] = ptx::f32x2(a.cap_n[u], a.cap_n[u]);
     }
     int tcount = 0;  // tiles of this slot so far (SFULL / PVDONE phases)
     bool ok = true;
@@ -617,20 +627,28 @@ __global__ void __launch_bounds__(384, 1)
         const bool masked = c0 < all_lo || c0 + BK > all_hi;  // warp-uniform
         // `raw_args`: s stays raw and the exp pass applies the scale or the
         // polynomial; otherwise s is brought to log2 units here
-        bool raw_args = true;
+        bool raw_args = true, narrow = false;
         float mx;
         if constexpr (CAP) {
           const float top = row_max(s), low = row_min(s);
-          const bool wide = __any_sync(0xffffffffu, fmaxf(top, -low) > a.cap_fast);
+          const float far = fmaxf(top, -low);
+          const bool wide = __any_sync(0xffffffffu, far > a.cap_fast);
+          narrow = !__any_sync(0xffffffffu, far > 0.5f * a.cap_fast);
           raw_args = !wide && !masked && !BIAS;
           if (raw_args) {
             float y0, y1;
             const uint64_t v = ptx::f32x2(top, top);
             ptx::f32x2_split(mul_f32x2(v, cap_poly(v, cap)), y0, y1);
-            mx = y0;  // the polynomial rises with s
+            mx = y0;  // the polynomials rise with s and agree to their error
           } else if (wide) {
 #pragma unroll
             for (int c = 0; c < BK; ++c) s[c] = a.cap_log2 * tanh_wide(s[c] * a.cap_in);
+          } else if (narrow) {
+#pragma unroll
+            for (int c = 0; c < BK; c += 2) {
+              const uint64_t v = ptx::f32x2(s[c], s[c + 1]);
+              ptx::f32x2_split(mul_f32x2(v, cap_poly_narrow(v, cap_n)), s[c], s[c + 1]);
+            }
           } else {
 #pragma unroll
             for (int c = 0; c < BK; c += 2) {
@@ -688,7 +706,7 @@ __global__ void __launch_bounds__(384, 1)
 #pragma unroll
               for (int e = 0; e < 16; ++e) pk[e] = 0u;
             } else {
-              scored_exp32<decltype(capped)::value>(s + 32 * c, mul2, negm2, cap, pk, acc0, acc1);
+              scored_exp32<decltype(capped)::value>(s + 32 * c, mul2, negm2, cap, cap_n, pk, acc0, acc1);
             }
             ptx::tmem_st32_16(lane_base + s_col + c * 16, pk);
             if ((c + 1) % CPP == 0 && c + 1 < BK / 32) {
@@ -700,13 +718,13 @@ __global__ void __launch_bounds__(384, 1)
             }
           }
         };
-        if constexpr (CAP) {
-          if (!BIAS && raw_args) exp_pass(std::true_type{}, one2);
-          else exp_pass(std::false_type{}, one2);
-        } else if constexpr (BIAS) {
-          exp_pass(std::false_type{}, one2);
+        using Plain = std::integral_constant<int, 0>;
+        if constexpr (CAP && !BIAS) {
+          if (raw_args && narrow) exp_pass(std::integral_constant<int, 1>{}, one2);
+          else if (raw_args) exp_pass(std::integral_constant<int, 2>{}, one2);
+          else exp_pass(Plain{}, one2);
         } else {
-          exp_pass(std::false_type{}, scale2);
+          exp_pass(Plain{}, BIAS ? one2 : scale2);
         }
         float a0, a1, b0, b1;
         ptx::f32x2_split(acc0, a0, a1);

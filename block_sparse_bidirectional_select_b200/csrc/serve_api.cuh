@@ -130,20 +130,24 @@ int launch_scored(const ScoredMaps& t, const ScoredArgs& a, bool cap, int dev, i
 }
 
 // Capped scores in log2 units: y = s * P(s^2) while |s| * scale / cap <= 0.5,
-// with tanh(u) = u * (c0 + c1 u^2 + c2 u^4 + c3 u^6) to 1.3e-7 there (minimax fit).
-void cap_coefficients(float scale, float softcap, float (&c)[4], float* fast, float* in, float* cap_log2) {
+// with tanh(u) = u * (c0 + c1 u^2 + c2 u^4 + c3 u^6) to 1.3e-7 there, and with
+// u * (n0 + n1 u^2 + n2 u^4) to 5e-8 while it is at most 0.25 (minimax fits).
+template <typename Args>
+void cap_coefficients(float scale, float softcap, Args* a) {
   constexpr double kC[4] = {0.9999976761831301, -0.3332065518031203, 0.1314514529551474, -0.04337247410609953};
+  constexpr double kN[3] = {0.9999986329824756, -0.33315701527853825, 0.12762231570462274};
   const double u = static_cast<double>(scale) / softcap, cl = softcap * 1.4426950408889634;
   double f = cl * u;
   bool finite = true;
   for (int i = 0; i < 4; ++i, f *= u * u) {
-    c[i] = static_cast<float>(kC[i] * f);
-    finite = finite && std::isfinite(c[i]);
+    a->cap_c[i] = static_cast<float>(kC[i] * f);
+    if (i < 3) a->cap_n[i] = static_cast<float>(kN[i] * f);
+    finite = finite && std::isfinite(a->cap_c[i]);
   }
-  *in = static_cast<float>(u);
-  *cap_log2 = static_cast<float>(cl);
+  a->cap_in = static_cast<float>(u);
+  a->cap_log2 = static_cast<float>(cl);
   // above this the wide form; everywhere if the polynomial does not fit fp32
-  *fast = !finite ? -1.f : (u > 0 && 0.5 / u < 1e18 ? static_cast<float>(0.5 / u) : 1e18f);
+  a->cap_fast = !finite ? -1.f : (u > 0 && 0.5 / u < 1e18 ? static_cast<float>(0.5 / u) : 1e18f);
 }
 
 // Partial results of cache_attn: two slots per CTA.
@@ -383,7 +387,7 @@ int sparsed_cache_attn(const uint16_t* Q, size_t q_stride_n, size_t q_stride_h, 
   if (a.scale_log2 < 1.17549435e-38f) a.scale_log2 = 1.17549435e-38f;  // as scored_attn
   a.slopes = slopes;
   const int mode = softcap > 0.f ? 2 : (slopes ? 1 : 0);
-  if (mode == 2) cap_coefficients(scale, softcap, a.cap_c, &a.cap_fast, &a.cap_in, &a.cap_log2);
+  if (mode == 2) cap_coefficients(scale, softcap, &a);
   a.o = O;
   a.lse = LSE;
   a.o_part = static_cast<float*>(workspace);
@@ -480,7 +484,7 @@ int sparsed_scored_attn(const uint16_t* Q, size_t q_stride_h, size_t q_stride_l,
   a.slopes = slopes;
   a.q_start = q_start;
   a.ranges = reinterpret_cast<const int2*>(ranges);
-  if (softcap > 0.f) cap_coefficients(scale, softcap, a.cap_c, &a.cap_fast, &a.cap_in, &a.cap_log2);
+  if (softcap > 0.f) cap_coefficients(scale, softcap, &a);
   a.lse = LSE;
   a.o = O;
   a.timeout_ns = kWaitTimeoutNs;
