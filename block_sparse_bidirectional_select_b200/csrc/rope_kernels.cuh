@@ -12,7 +12,9 @@
 // position * fraction in 64-bit integers drops whole turns exactly and the
 // upper 32 bits are the signed fraction of a turn. An fp32 product would be
 // off by position * 2^-24 (0.06 rad at a position of 10^6); this one is off by
-// 2^-32 turns plus position * 2^-53 at most.
+// 2^-32 turns plus position * 2^-53 at most, and fp32 by 2^-23 rad. Reduced to
+// [-pi, pi), the hardware sine and cosine are off by 2^-21, an eight-thousandth
+// of the result's rounding to bf16.
 #pragma once
 
 #include "ptx_sm100.cuh"
@@ -84,8 +86,10 @@ __global__ void __launch_bounds__(kRopeThreads) rope_axes_kernel(const __grid_co
     const int j = min(j0 + e, a.J - 1);
     const long p = a.pos[static_cast<long>(a.axis[j]) * a.L + l] * static_cast<long>(a.sign);
     const uint64_t turns = static_cast<uint64_t>(p) * a.turn[j];
-    // signed fraction of a turn -> half turns in [-1, 1)
-    sincospif(static_cast<float>(static_cast<int32_t>(turns >> 32)) * 0x1p-31f, &sn[e], &cs[e]);
+    // signed fraction of a turn -> radians in [-pi, pi)
+    const float t = static_cast<float>(static_cast<int32_t>(turns >> 32)) * (0x1p-32f * 6.283185307179586f);
+    sn[e] = __sinf(t);
+    cs[e] = __cosf(t);
   }
   if constexpr (VEC) {
     // the unit's two 16-byte parts
