@@ -748,9 +748,14 @@ def _launch(name, dev, stream, keep, args):
         raise SparsedError(rc, name)
 
 
+def _contiguous_like(x):
+    # half the time of new_empty
+    return torch.empty_like(x, memory_format=torch.contiguous_format)
+
+
 def _out_like(name, out, like, shape, dtype):
     if out is None:
-        return like.new_empty(shape, dtype=dtype)
+        return _contiguous_like(like) if dtype is like.dtype else like.new_empty(shape, dtype=dtype)
     _check_flat(name, out, dtype, shape)
     if out.device != like.device:
         raise ValueError(f"{name} must be on {like.device}")
@@ -789,7 +794,7 @@ def rope_axes(x, positions, sections, theta=10000.0, interleaved=False, shared_l
     _check_flat("positions", positions, torch.int32, (axes, L))
     if out is None:
         dev = _device_of(x, positions=positions)
-        out, ys = x.new_empty(shape), (L * d, d)
+        out, ys = _contiguous_like(x), (L * d, d)
     else:
         dev = _device_of(x, positions=positions, out=out)
         out_shape, ys = _strided("out", out, 3)

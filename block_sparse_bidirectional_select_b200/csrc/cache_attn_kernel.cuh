@@ -15,7 +15,10 @@
 // the same number of bytes. A CTA's run crosses item boundaries; an item cut by
 // a run's end leaves partial results (O normalised, log2 of the sum) that
 // cache_merge_kernel joins in the order of the runs: no atomics, the same bits
-// every time.
+// every time. Beginning an item (its Q, the last one's epilogue) costs a CTA
+// some 4 us, so each item counts `toll` tiles more than it has, ahead of its
+// first (kTollFew, kTollMany below): a CTA among many short items gets fewer
+// tiles.
 //
 // Exact operands. e4m3 has 4 significant bits and bf16 has 8, so a bf16 query
 // is the sum of two e4m3 numbers: hi = e4m3(q 2^-e), lo = e4m3(q 2^-e - hi),
@@ -64,6 +67,7 @@
 namespace sparsed {
 
 constexpr int kCacheMaxCtas = 160;
+constexpr int kTollFew = 8, kTollMany = 3;
 constexpr float kPShift = 7.0f;  // P's top is 2^7 when its row maximum is fresh
 
 struct CacheArgs {
@@ -76,6 +80,7 @@ struct CacheArgs {
   int R, RT;                       // rows of a kv head, row tiles
   int part_rows;                   // rows of a partial result's slot
   int tile;                        // keys of a tile
+  int toll;                        // what beginning an item costs, in tiles
   float scale_log2;                // above 0
   const float* slopes;             // or null
   float cap_c[4], cap_n[3];        // as ScoredArgs
@@ -226,11 +231,14 @@ __device__ __forceinline__ void reg_fence16(uint32_t (&r)[16]) {
 __device__ __forceinline__ int cache_len(const CacheArgs& a, int n) { return min(max(a.lengths[n], 0), a.C); }
 __device__ __forceinline__ int cache_tiles(const CacheArgs& a, int len) { return (len + a.tile - 1) / a.tile; }
 
-// Total key tiles of the call, and those before sequence n_stop (one warp).
+// An item's length in the runs' unit: its tiles and the toll.
+__device__ __forceinline__ int item_units(const CacheArgs& a, int nt) { return nt > 0 ? nt + a.toll : 0; }
+
+// Total units of the call, and those before sequence n_stop (one warp).
 __device__ __forceinline__ long cache_total(const CacheArgs& a, int lane, int n_stop, long* before) {
   long t = 0, b = 0;
   for (int n = lane; n < a.N; n += 32) {
-    const long x = static_cast<long>(cache_tiles(a, cache_len(a, n))) * a.Hkv * a.RT;
+    const long x = static_cast<long>(item_units(a, cache_tiles(a, cache_len(a, n)))) * a.Hkv * a.RT;
     t += x;
     if (n < n_stop) b += x;
   }
@@ -243,7 +251,7 @@ __device__ __forceinline__ long cache_total(const CacheArgs& a, int lane, int n_
   return t;
 }
 
-// First tile of run c of G runs over T tiles.
+// First unit of run c of G runs over T units.
 __device__ __forceinline__ long run_begin(long T, int c, int G) {
   const long q = T / G;
   return q * c + static_cast<int>(T - q * G) * c / G;
@@ -257,38 +265,44 @@ struct CachePart {
   int t0, cnt;     // this part's tiles
 };
 struct CacheRun {
-  int n, hk, rt, t;  // where the run stands: item, tile
+  int n, hk, rt, u;  // where the run stands: item, unit of it
   int len, nt;       // of sequence n
-  int left;          // tiles to go
+  int left;          // units to go
   __device__ __forceinline__ void load(const CacheArgs& a) {
     len = cache_len(a, n);
     nt = cache_tiles(a, len);
   }
   __device__ __forceinline__ bool next(const CacheArgs& a, CachePart& p) {
-    if (left <= 0) return false;
-    if (t >= nt) {  // the next item, past empty sequences
-      t = 0;
-      if (++rt >= a.RT) {
-        rt = 0;
-        if (++hk >= a.Hkv) {
-          hk = 0;
-          do {
-            if (++n >= a.N) return false;
-            load(a);
-          } while (nt == 0);
+    while (left > 0) {
+      if (u >= nt + a.toll) {  // the next item, past empty sequences
+        u = 0;
+        if (++rt >= a.RT) {
+          rt = 0;
+          if (++hk >= a.Hkv) {
+            hk = 0;
+            do {
+              if (++n >= a.N) return false;
+              load(a);
+            } while (nt == 0);
+          }
         }
       }
+      const int step = min(nt + a.toll - u, left);
+      const int t0 = max(u - a.toll, 0), t1 = max(u + step - a.toll, 0);
+      u += step;
+      left -= step;
+      if (t1 > t0) {  // not the toll alone
+        p.n = n;
+        p.hk = hk;
+        p.rt = rt;
+        p.len = len;
+        p.nt = nt;
+        p.t0 = t0;
+        p.cnt = t1 - t0;
+        return true;
+      }
     }
-    p.n = n;
-    p.hk = hk;
-    p.rt = rt;
-    p.len = len;
-    p.nt = nt;
-    p.t0 = t;
-    p.cnt = min(nt - t, left);
-    t += p.cnt;
-    left -= p.cnt;
-    return true;
+    return false;
   }
 };
 
@@ -350,7 +364,7 @@ __global__ void __launch_bounds__(CacheCfg<D, Q>::THREADS, 1)
   const int lane = threadIdx.x & 31;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::OFF_MISC);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::OFF_MISC + 4);
-  volatile int* run_s = reinterpret_cast<volatile int*>(smem + C::OFF_MISC + 8);  // sequence, item in it, tile, tiles
+  volatile int* run_s = reinterpret_cast<volatile int*>(smem + C::OFF_MISC + 8);  // sequence, item in it, unit, units
   auto bar = [&](int idx) -> uint32_t { return sb + C::OFF_BAR + 8 * idx; };
 
   // ---- setup
@@ -383,14 +397,14 @@ __global__ void __launch_bounds__(CacheCfg<D, Q>::THREADS, 1)
     ptx::tmem_relinquish();
   }
   if (warp == 12) {
-    // my run: its first tile's sequence, and the tile within the sequence
+    // my run: its first unit's sequence, and the unit within the sequence
     const long T = cache_total(a, lane, 0, nullptr);
     const long begin = run_begin(T, blockIdx.x, gridDim.x), end = run_begin(T, blockIdx.x + 1, gridDim.x);
     long base = 0;
     int n0 = a.N;
     for (int nb = 0; nb < a.N && begin < end; nb += 32) {
       const int n = nb + lane;
-      const long x = n < a.N ? static_cast<long>(cache_tiles(a, cache_len(a, n))) * a.Hkv * a.RT : 0;
+      const long x = n < a.N ? static_cast<long>(item_units(a, cache_tiles(a, cache_len(a, n)))) * a.Hkv * a.RT : 0;
       long inc = x;
 #pragma unroll
       for (int off = 1; off < 32; off <<= 1) {
@@ -408,11 +422,11 @@ __global__ void __launch_bounds__(CacheCfg<D, Q>::THREADS, 1)
     }
     if (lane == 0) {
       const bool some = n0 < a.N;
-      const int nt = some ? cache_tiles(a, cache_len(a, n0)) : 1;
+      const int units = some ? item_units(a, cache_tiles(a, cache_len(a, n0))) : 1;
       const long off = begin - base;
       run_s[0] = some ? n0 : 0;
-      run_s[1] = some ? static_cast<int>(off / nt) : 0;
-      run_s[2] = some ? static_cast<int>(off % nt) : 0;
+      run_s[1] = some ? static_cast<int>(off / units) : 0;
+      run_s[2] = some ? static_cast<int>(off % units) : 0;
       run_s[3] = some ? static_cast<int>(end - begin) : 0;
     }
   }
@@ -439,7 +453,7 @@ __global__ void __launch_bounds__(CacheCfg<D, Q>::THREADS, 1)
   run.n = run_s[0];
   run.hk = run_s[1] / a.RT;
   run.rt = run_s[1] - run.hk * a.RT;
-  run.t = run_s[2];
+  run.u = run_s[2];
   run.left = run_s[3];
   if (run.left > 0) run.load(a);
   CachePart part;
@@ -971,16 +985,19 @@ __global__ void __launch_bounds__(CacheCfg<D, Q>::THREADS, 1)
 #pragma unroll
             for (int c = 0; c < N; c += 2)
               ptx::f32x2_split(mul_f32x2(ptx::f32x2(s[c], s[c + 1]), f22), s[c], s[c + 1]);
+            // the polynomial while the warp's vote on it is under way
+            float y[N];
+#pragma unroll
+            for (int c = 0; c < N; c += 2) {
+              const uint64_t v = ptx::f32x2(s[c], s[c + 1]);
+              ptx::f32x2_split(mul_f32x2(v, cap_poly(v, cap)), y[c], y[c + 1]);
+            }
             if (__any_sync(0xffffffffu, fmaxf(row_max(s), -row_min(s)) > a.cap_fast)) {
 #pragma unroll
-              for (int c = 0; c < N; ++c) s[c] = a.cap_log2 * tanh_wide(s[c] * a.cap_in);
-            } else {
-#pragma unroll
-              for (int c = 0; c < N; c += 2) {
-                const uint64_t v = ptx::f32x2(s[c], s[c + 1]);
-                ptx::f32x2_split(mul_f32x2(v, cap_poly(v, cap)), s[c], s[c + 1]);
-              }
+              for (int c = 0; c < N; ++c) y[c] = a.cap_log2 * tanh_wide(s[c] * a.cap_in);
             }
+#pragma unroll
+            for (int c = 0; c < N; ++c) s[c] = y[c];
             f = 1.f;
             if (a.slopes) scale_and_bias(s, 1.f, slope2, at, t * C::BK + key0);
           }
@@ -1108,7 +1125,7 @@ __global__ void __launch_bounds__(kCacheMaxCtas) cache_merge_kernel(const __grid
   }
   long before;
   const long T = cache_total(a, lane, n, &before);
-  const long x0 = before + static_cast<long>(item) * nt, x1 = x0 + nt;  // the item's tiles
+  const long x0 = before + static_cast<long>(item) * item_units(a, nt) + a.toll, x1 = x0 + nt;  // the item's tiles
   const int c = threadIdx.x;
   const long b0 = run_begin(T, c, runs), b1 = c < runs ? run_begin(T, c + 1, runs) : b0;
   const bool holds = b0 < b1 && b0 < x1 && b1 > x0;

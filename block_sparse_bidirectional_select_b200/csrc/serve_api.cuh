@@ -181,11 +181,12 @@ template <int D, int MODE, int Q>
 int launch_cache_attn(const uint8_t* k8, const uint8_t* v8, CacheArgs& a, int dev, int sms, cudaStream_t st) {
   using C = CacheCfg<D, Q>;
   a.tile = C::BK;
+  a.toll = C::FEW ? kTollFew : kTollMany;
   const unsigned items = static_cast<unsigned>(a.Hkv) * static_cast<unsigned>(a.RT);
   if (sms > kCacheMaxCtas) sms = kCacheMaxCtas;
   // no more runs than there can be key tiles
   const long most = static_cast<long>(a.N) * items * cdiv(a.C, C::BK);
-  if (most / sms >= (1l << 30)) return SPARSED_ERR_UNSUPPORTED;
+  if (static_cast<long>(a.N) * items * (cdiv(a.C, C::BK) + a.toll) / sms >= (1l << 30)) return SPARSED_ERR_UNSUPPORTED;
   const int runs = static_cast<int>(most < sms ? most : sms);
   if (runs > 0) {
     auto kern = cache_attn_kernel<D, MODE, Q>;
