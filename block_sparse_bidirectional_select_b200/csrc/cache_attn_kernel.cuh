@@ -971,7 +971,7 @@ __global__ void __launch_bounds__(CacheCfg<D, Q>::THREADS, 1)
           if (lane == 0) ptx::mbar_arrive(bar(C::B_SREAD + b));
         }
         if (warp_on) {
-          float f = fminf(f2 * a.scale_log2, 1e37f);
+          float f = fminf(fmaxf(f2 * a.scale_log2, 1.17549435e-38f), 1e37f);  // 0 would turn a masked -inf into NaN
           // keys past the length, in an item's last tile only
           const int valid = part.len - t * C::BK - key0;
           const bool ragged = t == part.nt - 1;

@@ -144,7 +144,7 @@ void cap_coefficients(float scale, float softcap, Args* a) {
     if (i < 3) a->cap_n[i] = static_cast<float>(kN[i] * f);
     finite = finite && std::isfinite(a->cap_c[i]);
   }
-  a->cap_in = static_cast<float>(u);
+  a->cap_in = u < 3e38 ? static_cast<float>(u) : 3e38f;
   a->cap_log2 = static_cast<float>(cl);
   // above this the wide form; everywhere if the polynomial does not fit fp32
   a->cap_fast = !finite ? -1.f : (u > 0 && 0.5 / u < 1e18 ? static_cast<float>(0.5 / u) : 1e18f);
@@ -354,7 +354,7 @@ int sparsed_cache_attn(const uint16_t* Q, size_t q_stride_n, size_t q_stride_h, 
   if (d != 64 && d != 128) return SPARSED_ERR_UNSUPPORTED;
   if (N == 0 || Hq == 0 || B == 0) return SPARSED_OK;
   if (Hkv == 0 || Hq % Hkv != 0) return SPARSED_ERR_INVALID_ARG;
-  if (N > 65535 || Hq > 65535 || C > (1 << 29) || B > (1 << 24)) return SPARSED_ERR_UNSUPPORTED;
+  if (N > 16384 || Hq > 65535 || C > (1 << 29) || B > (1 << 24)) return SPARSED_ERR_UNSUPPORTED;
   if (!Q || !O || !LSE || !lengths || (C > 0 && (!k8 || !v8 || !k_scale || !v_scale))) return SPARSED_ERR_INVALID_ARG;
   if (!aligned16(Q) || !aligned16(k8) || !aligned16(v8) || !aligned16(O) || !aligned4(LSE) || !aligned4(lengths) ||
       !aligned4(q_start) || !aligned4(k_scale) || !aligned4(v_scale))

@@ -561,7 +561,8 @@ int sparsed_losa_block(const uint16_t* Qs, const uint16_t* Ks, const uint16_t* V
  * attention with modified scores. These entry points take strided inputs, so
  * that heads can be read where a projection wrote them: a stride is counted in
  * elements, and the d elements of a head row are contiguous. Outputs are
- * written whole by every call. */
+ * written whole by every call and must not overlap inputs unless stated. The
+ * current device is the one the pointers and the stream belong to. */
 
 /* Rotary positions with n_axes axes (for example time, height and width).
  * X and Y are [H, L, d] bf16 with the given strides; Y may be X with the same
@@ -627,7 +628,7 @@ int sparsed_cache_attn_workspace_bytes(int N, int Hq, int Hkv, int B, int d, siz
  * sequence's first query token. Cached bytes past lengths[n] are never used,
  * whatever they hold. length 0 gives O = 0 and LSE = -inf. LSE and O merge
  * with attention over other keys by the two-part LSE identity. softcap >= 0,
- * scale >= 0. Results do not depend on what else is in the batch up to
+ * scale >= 0, N <= 16384. Results do not depend on what else is in the batch up to
  * rounding, and are the same bits on every call with the same lengths.
  * workspace: sparsed_cache_attn_workspace_bytes, 256-byte aligned, contents
  * ignored; one workspace must not serve two calls at the same time. */
@@ -659,7 +660,10 @@ int sparsed_scored_attn_workspace_bytes(int Hq, int Lq, size_t* bytes);
  *   x = x - slopes[h] * |q_start + r - c|   if slopes is given (DEVICE [Hq] fp32)
  *   O[h,r,:] = sum_c softmax(x)_c v_c  (bf16 [Hq, Lq, d]),
  *   LSE[h,r] = ln sum_c exp(x)         (fp32 [Hq, Lq])
- * A row that sees nothing gives O = 0 and LSE = -inf. scale >= 0, softcap >= 0.
+ * A row that sees nothing gives O = 0 and LSE = -inf. What K and V hold at keys
+ * that no row sees has no effect; a NaN or infinity in V at a key that some row
+ * of the 256 rows 256 i .. 256 i + 255 of a head sees reaches all of those.
+ * scale >= 0, softcap >= 0, |q_start| <= 2^29.
  * workspace: sparsed_scored_attn_workspace_bytes, 256-byte aligned, contents
  * ignored; one workspace must not serve two calls at the same time. */
 int sparsed_scored_attn(const uint16_t* Q, size_t q_stride_h, size_t q_stride_l,

@@ -284,6 +284,79 @@ def test_cache_attn_strided_queries_other_stream_and_graph():
         assert torch.equal(out, w2) and torch.equal(out_lse, l2)
 
 
+def test_cache_attn_far_into_a_long_cache():
+    """Offsets past 2^32 bytes: the second sequence's last tokens lie beyond them."""
+    C, d = 17_000_000 // 64 * 64, 128
+    g = gen(25)
+    c = sp.cache_alloc(2, 1, C, d)
+    k, v = randn(g, 2, 1, 200, d), randn(g, 2, 1, 200, d)
+    starts = [0, C - 200]
+    sp.cache_append(c, k, v, i32(starts))
+    sp.device_check()
+    for x, x8, sc in ((k, c.k8, c.k_scale), (v, c.v8, c.v_scale)):
+        lo = C - 256
+        r8, rs = R.append(x[1:].cpu(), torch.zeros(1, 1, 256, d).to(torch.float8_e4m3fn), torch.full((1, 1, 4), 2.0 ** -117), [56], [200])
+        assert torch.equal(x8[1:, :, lo + 56:].cpu().view(torch.uint8), r8[:, :, 56:].view(torch.uint8))
+        assert torch.equal(sc[1:, :, -4:].cpu(), rs)
+    q = randn(g, 2, 2, 3, d)
+    slopes = torch.tensor([1.0, 0.5], device="cuda")
+    o, lse = sp.cache_attn(q, c, i32([200, C]), slopes=slopes)
+    sp.device_check()
+    # a slope of 0.5 leaves nothing of keys over 4096 tokens away
+    for n, (a, b) in enumerate(((0, 256), (C - 4096, C))):
+        L = 200 if n == 0 else 4096
+        kd, vd = (R.dequant(t8[n:n + 1, :, a:b], sc[n:n + 1, :, a // 64:b // 64])[0, 0, :L]
+                  for t8, sc in ((c.k8, c.k_scale), (c.v8, c.v_scale)))
+        at = torch.arange(L - 3, L, device="cuda")
+        lo = torch.zeros(3, dtype=torch.long, device="cuda")
+        for h in range(2):
+            ref = R.attend(q[n, h], kd, vd, lo, lo + L, at, sp.default_scale(d), 0.0, float(slopes[h]))
+            R.assert_attention(o[n, h], lse[n, h], ref, f"n={n} h={h}")
+
+
+def test_cache_attn_two_calls_at_once_and_a_spoiled_row():
+    """Calls on two streams with workspaces of their own, and a NaN or infinite query that spoils its own row only."""
+    g = gen(26)
+    c = random_cache(g, 4, 2, 4096, 128)
+    lengths = i32([4096, 17, 0, 2500])
+    qs = [randn(g, 4, 4, b, 128) for b in (1, 40)]
+    want = [sp.cache_attn(q, c, lengths, softcap=20.0) for q in qs]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in qs]
+    got = [None, None]
+    for _ in range(5):
+        for i, (q, s) in enumerate(zip(qs, streams)):
+            with torch.cuda.stream(s):
+                got[i] = sp.cache_attn(q, c, lengths, softcap=20.0)
+    torch.cuda.synchronize()
+    for (o, l), (wo, wl) in zip(got, want):
+        assert torch.equal(o, wo) and torch.equal(l, wl)
+    q = qs[1].clone()
+    q[0, 1, 7, 3], q[3, 2, 0, 0] = math.nan, math.inf
+    o, l = sp.cache_attn(q, c, lengths, softcap=20.0)
+    for n, h, b in ((0, 1, 7), (3, 2, 0)):
+        assert torch.isnan(o[n, h, b]).all() and torch.isnan(l[n, h, b])
+        o[n, h, b], l[n, h, b] = want[1][0][n, h, b], want[1][1][n, h, b]
+    assert torch.equal(o, want[1][0]) and torch.equal(l, want[1][1])
+
+
+def test_zero_and_extreme_options():
+    g = gen(27)
+    c = random_cache(g, 1, 1, 192, 64)
+    q = randn(g, 1, 2, 2, 64)
+    check_cache_attn(q, c, [130], scale=0.0)
+    check_cache_attn(q, c, [130], softcap=1e-30)
+    check_cache_attn(q, c, [130], softcap=1e30)
+    k, v = randn(g, 1, 130, 64), randn(g, 1, 130, 64)
+    r = torch.tensor([[5, 100], [129, 130]], dtype=torch.int32, device="cuda")
+    for kw in (dict(scale=0.0), dict(softcap=1e-30), dict(softcap=1e30), dict(scale=0.0, softcap=5.0, slopes=slopes_of(2))):
+        check_scored(q[0], k, v, ranges=r, **kw)
+    o, lse = sp.scored_attn(q[0], k[:, :0], v[:, :0])
+    assert (o == 0).all() and torch.isneginf(lse).all()
+    o, lse = sp.cache_attn(q, sp.cache_alloc(1, 1, 0, 64), i32([0]))
+    assert (o == 0).all() and torch.isneginf(lse).all()
+
+
 # ------------------------------------------------------------------ dense attention with modified scores
 
 def check_scored(q, k, v, softcap=0.0, slopes=None, ranges=None, q_start=0, scale=None, what=""):
