@@ -699,9 +699,9 @@ def _device_of(first, **tensors):
     dev = first.device
     if dev.type != "cuda":
         raise ValueError("tensors must be on a CUDA device")
-    for name, t in tensors.items():
+    for t in tensors.values():
         if t is not None and t.device != dev:
-            raise ValueError(f"{name} must be on {dev}, got {t.device}")
+            raise ValueError(f"{', '.join(tensors)} must be on {dev}, got {t.device}")
     return dev
 
 
@@ -832,11 +832,18 @@ def _check_cache(cache):
         raise ValueError(f"the cache must be [N, Hkv, C, d] with C a multiple of {CACHE_BLOCK}, got {tuple(shape)}")
     N, H, C, d = shape
     blocks = (N, H, C // CACHE_BLOCK)
-    _check_flat("k8", k8, torch.float8_e4m3fn, shape)
-    _check_flat("v8", v8, torch.float8_e4m3fn, shape)
-    _check_flat("k_scale", ks, torch.float32, blocks)
-    _check_flat("v_scale", vs, torch.float32, blocks)
-    return N, H, C, d, _device_of(k8, v8=v8, k_scale=ks, v_scale=vs)
+    dev, f8, f32 = k8.device, torch.float8_e4m3fn, torch.float32
+    if not (k8.dtype is f8 and v8.dtype is f8 and ks.dtype is f32 and vs.dtype is f32 and v8.shape == shape
+            and ks.shape == blocks and vs.shape == blocks and k8.is_contiguous() and v8.is_contiguous()
+            and ks.is_contiguous() and vs.is_contiguous() and dev.type == "cuda" and v8.device == dev
+            and ks.device == dev and vs.device == dev):
+        # what is wrong with it
+        _check_flat("k8", k8, f8, shape)
+        _check_flat("v8", v8, f8, shape)
+        _check_flat("k_scale", ks, f32, blocks)
+        _check_flat("v_scale", vs, f32, blocks)
+        _device_of(k8, v8=v8, k_scale=ks, v_scale=vs)
+    return N, H, C, d, dev
 
 
 def cache_append(cache: Cache8, k, v, start, count=None, stream=None) -> Cache8:
