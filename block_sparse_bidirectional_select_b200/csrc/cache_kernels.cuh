@@ -109,14 +109,24 @@ __global__ void __launch_bounds__(256) cache_append_kernel(const __grid_constant
     }
   }
   const float held = *scale;  // of a block that holds older tokens
+  // magnitudes as 16-bit integers, two to a word (two operations for two values)
 #pragma unroll
   for (int p = 0; p < NP; ++p) {
     const uint32_t w[4] = {v[p].x, v[p].y, v[p].z, v[p].w};
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const uint32_t lo = w[e] & 0x7FFFu, hi = (w[e] >> 16) & 0x7FFFu;
-      mx = max(mx, lo < 0x7F80u ? lo : 0u);  // the maximum of the finite values
-      mx = max(mx, hi < 0x7F80u ? hi : 0u);
+    for (int e = 0; e < 4; ++e) mx = __vmaxu2(mx, w[e] & 0x7FFF7FFFu);
+  }
+  mx = max(mx & 0xFFFFu, mx >> 16);
+  if (mx >= 0x7F80u) {  // an infinity or NaN among them: the maximum of the finite ones
+    mx = 0;
+#pragma unroll
+    for (int p = 0; p < NP; ++p) {
+      const uint32_t w[4] = {v[p].x, v[p].y, v[p].z, v[p].w};
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const uint32_t lo = w[e] & 0x7FFFu, hi = (w[e] >> 16) & 0x7FFFu;
+        mx = max(mx, max(lo < 0x7F80u ? lo : 0u, hi < 0x7F80u ? hi : 0u));
+      }
     }
   }
   mx = __reduce_max_sync(0xffffffffu, mx);
