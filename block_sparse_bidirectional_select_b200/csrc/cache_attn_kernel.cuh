@@ -999,10 +999,11 @@ __global__ void __launch_bounds__(CacheCfg<D, Q>::THREADS, 1)
 #pragma unroll
             for (int c = 0; c < N; ++c) s[c] = y[c];
             f = 1.f;
-            if (a.slopes) scale_and_bias(s, 1.f, slope2, at, t * C::BK + key0);
+            if (a.slopes) scale_and_bias(s, [](uint64_t) { return ptx::f32x2(1.f, 1.f); }, slope2, at, t * C::BK + key0);
           }
           if constexpr (MODE == 1) {
-            scale_and_bias(s, f, slope2, at, t * C::BK + key0);
+            const uint64_t ff = ptx::f32x2(f, f);
+            scale_and_bias(s, [&](uint64_t) { return ff; }, slope2, at, t * C::BK + key0);
             f = 1.f;
           }
           if (ragged) {

@@ -108,23 +108,26 @@ __device__ __forceinline__ uint64_t cap_poly(uint64_t s, const uint64_t (&c)[4])
   return ptx::fma_f32x2(p, w, c[0]);
 }
 
-// s[0..N) = s * mul - slope2 * |at - c| for the N consecutive keys c from c0 on,
-// in log2 units. Distances are exact in fp32 up to 2^24; |at - c| is linear in
-// the key where a warp's keys all lie on one side of each thread's row: then
-// eight keys share a base and four pairs of offsets, two packed operations for
-// two scores.
-template <int N>
-__device__ __forceinline__ void scale_and_bias(float (&s)[N], float mul, float slope2, int at, int c0) {
+// s[0..N) = s * mul(s) - slope2 * |at - c| for the N consecutive keys c from c0
+// on, in log2 units; mul: of a pair of scores, the scale or a cap polynomial.
+// Distances are exact in fp32 up to 2^24; |at - c| is linear in the key where a
+// warp's keys all lie on one side of each thread's row: then eight keys share
+// a base and four pairs of offsets, two packed operations for two scores.
+template <int N, typename Mul>
+__device__ __forceinline__ void scale_and_bias(float (&s)[N], Mul mul, float slope2, int at, int c0) {
   const float d0 = static_cast<float>(at - c0);
   if (__any_sync(0xffffffffu, at > c0 && at < c0 + N - 1)) {
 #pragma unroll
-    for (int e = 0; e < N; ++e) s[e] = fmaf(-slope2, fabsf(d0 - static_cast<float>(e)), s[e] * mul);
+    for (int e = 0; e < N; e += 2) {
+      const uint64_t v = ptx::f32x2(s[e], s[e + 1]);
+      const uint64_t t = ptx::f32x2(-slope2 * fabsf(d0 - static_cast<float>(e)), -slope2 * fabsf(d0 - static_cast<float>(e + 1)));
+      ptx::f32x2_split(ptx::fma_f32x2(v, mul(v), t), s[e], s[e + 1]);
+    }
   } else {
     const float b1 = at > c0 ? slope2 : -slope2;  // per key: keys left of the row come nearer
     uint64_t off[4];
 #pragma unroll
     for (int u = 0; u < 4; ++u) off[u] = ptx::f32x2(b1 * (2 * u), b1 * (2 * u + 1));
-    const uint64_t mul2 = ptx::f32x2(mul, mul);
     const float b0 = -slope2 * fabsf(d0);
 #pragma unroll
     for (int q = 0; q < N / 8; ++q) {
@@ -133,8 +136,8 @@ __device__ __forceinline__ void scale_and_bias(float (&s)[N], float mul, float s
 #pragma unroll
       for (int u = 0; u < 4; ++u) {
         const int e = 8 * q + 2 * u;
-        ptx::f32x2_split(ptx::fma_f32x2(ptx::f32x2(s[e], s[e + 1]), mul2, ptx::add_f32x2(base2, off[u])), s[e],
-                         s[e + 1]);
+        const uint64_t v = ptx::f32x2(s[e], s[e + 1]);
+        ptx::f32x2_split(ptx::fma_f32x2(v, mul(v), ptx::add_f32x2(base2, off[u])), s[e], s[e + 1]);
       }
     }
   }
@@ -643,12 +646,10 @@ __global__ void __launch_bounds__(384, 1)
           } else if (wide) {
 #pragma unroll
             for (int c = 0; c < BK; ++c) s[c] = a.cap_log2 * tanh_wide(s[c] * a.cap_in);
-          } else if (narrow) {
-#pragma unroll
-            for (int c = 0; c < BK; c += 2) {
-              const uint64_t v = ptx::f32x2(s[c], s[c + 1]);
-              ptx::f32x2_split(mul_f32x2(v, cap_poly_narrow(v, cap_n)), s[c], s[c + 1]);
-            }
+            if constexpr (BIAS) scale_and_bias(s, [&](uint64_t) { return one2; }, slope2, at, c0);
+          } else if constexpr (BIAS) {
+            if (narrow) scale_and_bias(s, [&](uint64_t v) { return cap_poly_narrow(v, cap_n); }, slope2, at, c0);
+            else scale_and_bias(s, [&](uint64_t v) { return cap_poly(v, cap); }, slope2, at, c0);
           } else {
 #pragma unroll
             for (int c = 0; c < BK; c += 2) {
@@ -656,10 +657,9 @@ __global__ void __launch_bounds__(384, 1)
               ptx::f32x2_split(mul_f32x2(v, cap_poly(v, cap)), s[c], s[c + 1]);
             }
           }
-        }
-        if constexpr (BIAS) {
+        } else if constexpr (BIAS) {
           raw_args = false;
-          scale_and_bias(s, CAP ? 1.f : a.scale_log2, slope2, at, c0);
+          scale_and_bias(s, [&](uint64_t) { return scale2; }, slope2, at, c0);
         }
         if (masked) {
 #pragma unroll
