@@ -22,7 +22,9 @@
 //   * with ranges, warp 11 clears the V rows of a tile that no row of the pair
 //     sees, so that whatever padding holds (0 * NaN) stays out of O. It looks
 //     closer only at tiles that no single row sees whole;
-//   * when the pairs would leave SMs idle, a CTA takes single query tiles.
+//   * when the pairs would leave SMs idle (`split`), a CTA takes one query tile, and
+//     its two slots the even and the odd key tiles of it; slot 0 joins their
+//     sums and outputs at the end.
 //
 // Capped scores. tanh(u) = u * P(u^2), P by a minimax fit (the coefficients are
 // scaled on the host so that the polynomial takes the raw product and gives
@@ -49,7 +51,7 @@ namespace sparsed {
 struct ScoredArgs {
   int H, group;             // query heads, query heads per kv head
   int L, Lk;                // query rows, keys
-  int nqb, qpp;             // query tiles of 128 rows per head; tiles per CTA and turn (1 or 2)
+  int nqb, qpp;             // query tiles of 128 rows per head; tiles per turn (2, or 1: split, one turn per CTA)
   float scale_log2;         // scale * log2(e), above 0
   const float* slopes;      // [H] or null
   int q_start;
@@ -70,10 +72,12 @@ struct ScoredCfg {
   using A = AttnCfg<D, BK>;
   static constexpr int NST = A::NST;
   static constexpr int B_VOK = A::NUM_BARS;           // [NST] V tile cleared of unseen rows
-  static constexpr int NUM_BARS = B_VOK + NST;
+  static constexpr int B_JOIN = B_VOK + NST;          // split: slot 1's sums are in shared memory, 4 warp arrivals
+  static constexpr int NUM_BARS = B_JOIN + 1;
   static constexpr int N_WTAKERS = A::N_WTAKERS + 1;  // and warp 11
   static constexpr int OFF_MISC = A::OFF_BAR + NUM_BARS * 8;  // tmem slot, abort flag, 2 x (pair, first tile, tiles, near)
-  static constexpr int SMEM_BYTES = OFF_MISC + 48 + 1024;
+  static constexpr int OFF_JOIN = (OFF_MISC + 48 + 15) & ~15;  // split: (max, sum) of slot 1's rows
+  static constexpr int SMEM_BYTES = OFF_JOIN + 128 * 8 + 1024;
   static_assert(SMEM_BYTES <= A::SMEM_LIMIT, "shared memory budget");
 };
 
@@ -233,7 +237,7 @@ __device__ __forceinline__ int2 scored_range(const ScoredArgs& a, int r, bool ou
   return v;
 }
 
-template <int D, bool CAP, bool BIAS>
+template <int D, bool CAP, bool BIAS, bool SPLIT>
 __global__ void __launch_bounds__(384, 1)
     scored_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                        const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ ScoredArgs a) {
@@ -249,6 +253,7 @@ __global__ void __launch_bounds__(384, 1)
   const int lane = threadIdx.x & 31;
   const int nph = (a.nqb + a.qpp - 1) / a.qpp;
   const int n_pairs = a.H * nph;
+  constexpr bool split = SPLIT;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + S::OFF_MISC);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + S::OFF_MISC + 4);
   // the producer publishes each turn here, double-buffered: pair, first key
@@ -274,6 +279,7 @@ __global__ void __launch_bounds__(384, 1)
       ptx::mbar_init(bar(C::B_EMPTY + s), a.ranges ? 3 : 2);  // two commits per tile, and warp 11
       ptx::mbar_init(bar(S::B_VOK + s), 1);
     }
+    ptx::mbar_init(bar(S::B_JOIN), 4);
     *abort_flag = 0;
     ptx::fence_mbar_init();
   }
@@ -393,7 +399,7 @@ __global__ void __launch_bounds__(384, 1)
           if (j == 0) ok = load_q(0, pr.q0);
           const int blk = j0 + (BIAS ? scored_tile(j, near) : j);
           if (ok) ok = load_tile(&tm_k, blk);
-          if (ok && pr.has1 && j == 0) ok = load_q(1, pr.q0 + 1);
+          if (ok && j == 0 && (split ? nj > 1 : pr.has1)) ok = load_q(1, split ? pr.q0 : pr.q0 + 1);
           if (ok) ok = load_tile(&tm_v, blk);
         }
         w = w_next;
@@ -434,13 +440,13 @@ __global__ void __launch_bounds__(384, 1)
         if (lane == 0) ptx::mbar_arrive(bar(C::B_WEMPTY + (np & 1)));
         if (w >= n_pairs) break;
         const ScoredPair pr = scored_pair(a, w, nph);
-        const bool mine = s == 0 || pr.has1;
-        const bool sole = !pr.has1;
+        const bool sole = !pr.has1;       // a tile has one slot, which gives both commits
+        const int first = split ? s : 0;  // my first tile
         for (int j = 0; j < nj; ++j) {
           const int sk = seq, sv = seq + 1;
           seq += 2;
-          if (!mine) continue;
-          if ((j == 0 && !wait(C::B_QFULL + s, qn++)) || !wait(C::B_FULL + sk % NST, sk / NST)) {
+          if (split ? (j & 1) != s : (s == 1 && !pr.has1)) continue;
+          if ((j == first && !wait(C::B_QFULL + s, qn++)) || !wait(C::B_FULL + sk % NST, sk / NST)) {
             ok = false;
             break;
           }
@@ -457,7 +463,7 @@ __global__ void __launch_bounds__(384, 1)
           commit(C::B_SFULL + s);
           commit(C::B_EMPTY + sk % NST);
           if (sole) commit(C::B_EMPTY + sk % NST);
-          if (j == nj - 1) commit(C::B_QEMPTY + s);
+          if (j + (split ? 2 : 1) >= nj) commit(C::B_QEMPTY + s);
           // with ranges, the V tile once warp 11 has passed it
           if (!wait(C::B_FULL + sv % NST, sv / NST) || (a.ranges && !wait(S::B_VOK + sv % NST, sv / NST))) {
             ok = false;
@@ -475,7 +481,7 @@ __global__ void __launch_bounds__(384, 1)
             for (int u = 0; u < KPP; ++u) {
               const int kk = q * KPP + u;
               ptx::umma_ts_lohi_if(leader, o_tmem, s_tmem + kk * 8, vb + kk * (2048 >> 4), HI, C::IDESC_PV,
-                                   (j > 0 || kk > 0) ? 1u : 0u);
+                                   (j > first || kk > 0) ? 1u : 0u);
             }
           }
           if (!ok) break;
@@ -597,8 +603,8 @@ __global__ void __launch_bounds__(384, 1)
       if (w >= n_pairs) break;
       const ScoredPair pr = scored_pair(a, w, nph);
       const int h = pr.h;
-      const int qi = pr.q0 + slot;
-      if (slot == 1 && !pr.has1) continue;
+      const int qi = split ? pr.q0 : pr.q0 + slot;
+      if (slot == 1 && (split ? nj == 0 : !pr.has1)) continue;
       const int grow = qi * 128 + r;
       const bool row_valid = grow < a.L;
       uint4* o_dst = reinterpret_cast<uint4*>(a.o + (static_cast<long>(h) * a.L + grow) * D);
@@ -611,7 +617,8 @@ __global__ void __launch_bounds__(384, 1)
       const int at = a.q_start + grow;
       float m = ninf;  // running row max, log2 units
       float l = 0.f;   // running row sum
-      for (int jj = 0; jj < nj; ++jj, ++tcount) {
+      const int first = split ? slot : 0, step = split ? 2 : 1;  // my tiles
+      for (int jj = first; jj < nj; jj += step, ++tcount) {
         const int c0 = (j0 + (BIAS ? scored_tile(jj, near) : jj)) * BK;
         if (!ptx::mbar_wait_warp(bar(C::B_SFULL + slot), tcount & 1, abort_flag, a.timeout_ns, kErrTimeout)) {
           ok = false;
@@ -677,7 +684,7 @@ __global__ void __launch_bounds__(384, 1)
           if constexpr (!BIAS) mx *= a.scale_log2;  // scale_log2 > 0
         }
         const float m_new = fmaxf(m, mx);
-        if (jj == 0) {
+        if (jj == first) {
           m = m_new;
         } else if (__any_sync(0xffffffffu, m_new > m + 8.0f)) {
           // O_s holds every earlier tile of this item: rescale my row (a row
@@ -749,24 +756,61 @@ __global__ void __launch_bounds__(384, 1)
         continue;
       }
       // ---- epilogue: every PV of the item is done -> O / l -> bf16 -> global; LSE
-      if (!ptx::mbar_wait_warp(bar(C::B_PVDONE + slot), (tcount - 1) & 1, abort_flag, a.timeout_ns, kErrTimeout)) {
+      if (tcount > 0 && !ptx::mbar_wait_warp(bar(C::B_PVDONE + slot), (tcount - 1) & 1, abort_flag, a.timeout_ns,
+                                             kErrTimeout)) {
         ok = false;
         break;
       }
       ptx::tc_fence_after();
+      float own = 1.f, other = 0.f;  // split: weights of both slots' outputs
+      if constexpr (split) {
+        float2* ml = reinterpret_cast<float2*>(smem + S::OFF_JOIN);
+        if (slot == 1) {
+          ml[r] = make_float2(m, l);
+          ptx::tc_fence_before();
+          __syncwarp();
+          if (lane == 0) ptx::mbar_arrive(bar(S::B_JOIN));
+          continue;
+        }
+        const int n1 = nj >> 1;  // slot 1's tiles
+        if (!ptx::mbar_wait_warp(bar(S::B_JOIN), 0, abort_flag, a.timeout_ns, kErrTimeout) ||
+            (n1 > 0 && !ptx::mbar_wait_warp(bar(C::B_PVDONE + 1), (n1 - 1) & 1, abort_flag, a.timeout_ns, kErrTimeout))) {
+          ok = false;
+          break;
+        }
+        ptx::tc_fence_after();
+        if (n1 > 0) {
+          const float2 x = ml[r];
+          const float M = fmaxf(m, x.x);
+          own = m == ninf && M != ninf ? 0.f : (m == M ? 1.f : ptx::ex2(m - M));
+          other = x.x == M ? 1.f : (x.x == ninf ? 0.f : ptx::ex2(x.x - M));
+          l = l * own + x.y * other;
+          m = M;
+        }
+      }
       const bool empty = l == 0.f;  // the row saw nothing
       const float inv_l = empty ? 0.f : 1.0f / l;
+      const bool two = split && __any_sync(0xffffffffu, other != 0.f);
+      const float f0 = own * inv_l, f1 = other * inv_l;
 #pragma unroll
       for (int c = 0; c < D / 32; ++c) {
         uint32_t raw[32];
         ptx::tmem_ld32(lane_base + o_col + c * 32, raw);
         ptx::tmem_wait_ld();
         ptx::reg_fence32(raw);
+        float v[32];
+#pragma unroll
+        for (int e = 0; e < 32; ++e) v[e] = f0 == 0.f ? 0.f : __uint_as_float(raw[e]) * f0;
+        if (two) {
+          ptx::tmem_ld32(lane_base + C::TM_O1 + c * 32, raw);
+          ptx::tmem_wait_ld();
+          ptx::reg_fence32(raw);
+#pragma unroll
+          for (int e = 0; e < 32; ++e) v[e] += f1 == 0.f ? 0.f : __uint_as_float(raw[e]) * f1;
+        }
         uint32_t pk[16];
 #pragma unroll
-        for (int e = 0; e < 16; ++e)
-          pk[e] = empty ? 0u
-                        : ptx::pack_bf16x2(__uint_as_float(raw[2 * e]) * inv_l, __uint_as_float(raw[2 * e + 1]) * inv_l);
+        for (int e = 0; e < 16; ++e) pk[e] = ptx::pack_bf16x2(v[2 * e], v[2 * e + 1]);
         if (row_valid) {
 #pragma unroll
           for (int u = 0; u < 4; ++u)

@@ -419,6 +419,38 @@ def test_scored_documents_and_prefixes(softcap, bias):
         check_scored(q, k, v, softcap, slopes, r)
 
 
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("softcap,bias,masked", [(0.0, False, False), (0.0, False, True), (9.0, False, True),
+                                                 (0.0, True, True), (9.0, True, False), (40.0, False, False)])
+def test_scored_more_query_tiles_than_sms(d, softcap, bias, masked):
+    """Pairs of query tiles and turns claimed from the counter: 40 heads of 6 tiles, odd tails."""
+    g = gen(45 + d)
+    L = 700
+    q, k, v = randn(g, 40, L, d, scale=2.0), randn(g, 8, L, d), randn(g, 8, L, d)
+    ranges = None
+    if masked:
+        ranges = sp.document_ranges(i32([0, 3, 260, 300, 655]), L, i32([0, 50, 1000, 120]))   # 45 rows see nothing
+        ranges[400:420] = 0
+    check_scored(q, k, v, softcap, slopes_of(40) if bias else None, ranges)
+
+
+def test_scored_padding_in_pairs_may_hold_anything():
+    g = gen(46)
+    L = 700
+    q, k, v = randn(g, 40, L, 64), randn(g, 4, L, 64), randn(g, 4, L, 64)
+    ranges = torch.zeros(L, 2, dtype=torch.int32)
+    ranges[:300] = torch.tensor([0, 300], dtype=torch.int32)
+    ranges[420:690] = torch.tensor([420, 690], dtype=torch.int32)
+    ranges = ranges.cuda()
+    want = sp.scored_attn(q, k, v, ranges=ranges)
+    for x in (k, v):
+        x[:, 300:420] = math.nan
+        x[:, 690:] = math.inf
+    got = sp.scored_attn(q, k, v, ranges=ranges)
+    assert torch.equal(want[0], got[0]) and torch.equal(want[1], got[1])
+    sp.device_check()
+
+
 def test_scored_arbitrary_ranges_and_empty_rows():
     """Ranges in any order, beyond the keys, reversed and empty; whole tiles of empty rows."""
     g = gen(42)
