@@ -201,6 +201,8 @@ def check_cache_attn(q, c, lengths, softcap=0.0, slopes=None, q_start=None, scal
     (5, 15, 1, 1, 2048, [2048, 1, 0, 2047, 64]),
     (40, 2, 2, 1, 128, [1 + (37 * n) % 128 for n in range(40)]),   # several items to a run
     (33, 1, 1, 20, 64, [20 + n for n in range(33)]),
+    (300, 1, 1, 1, 128, [(n * 53) % 129 for n in range(300)]),     # many sequences, some of them empty
+    (5, 4, 2, 70, 384, [0, 70, 384, 129, 200]),
 ])
 def test_cache_attn(d, N, Hq, Hkv, B, C, lengths):
     g = gen(N + Hq * 10 + B)
