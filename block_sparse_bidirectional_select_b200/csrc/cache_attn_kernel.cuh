@@ -1050,20 +1050,14 @@ __global__ void __launch_bounds__(CacheCfg<D, Q>::THREADS, 1)
           const uint64_t f2x = ptx::f32x2(f, f), neg2 = ptx::f32x2(neg, neg);
           uint64_t acc0 = ptx::f32x2(0.f, 0.f), acc1 = acc0;
           uint32_t pk[N / 2];
-          // with a steep bias whole tiles lie where 2^x is exactly 0
-          if (MODE != 0 && !__any_sync(0xffffffffu, !(mx + neg < -127.f))) {
 #pragma unroll
-            for (int e = 0; e < N / 2; ++e) pk[e] = 0u;
-          } else {
-#pragma unroll
-            for (int e = 0; e < N / 2; ++e) {
-              float x0, x1;
-              ptx::f32x2_split(ptx::fma_f32x2(ptx::f32x2(s[2 * e], s[2 * e + 1]), f2x, neg2), x0, x1);
-              const float p0 = ptx::ex2(x0), p1 = ptx::ex2(x1);
-              if (e & 1) acc1 = ptx::add_f32x2(acc1, ptx::f32x2(p0, p1));
-              else acc0 = ptx::add_f32x2(acc0, ptx::f32x2(p0, p1));
-              pk[e] = ptx::pack_f16x2(p0, p1);
-            }
+          for (int e = 0; e < N / 2; ++e) {
+            float x0, x1;
+            ptx::f32x2_split(ptx::fma_f32x2(ptx::f32x2(s[2 * e], s[2 * e + 1]), f2x, neg2), x0, x1);
+            const float p0 = ptx::ex2(x0), p1 = ptx::ex2(x1);
+            if (e & 1) acc1 = ptx::add_f32x2(acc1, ptx::f32x2(p0, p1));
+            else acc0 = ptx::add_f32x2(acc0, ptx::f32x2(p0, p1));
+            pk[e] = ptx::pack_f16x2(p0, p1);
           }
           float a0, a1, b0, b1;
           ptx::f32x2_split(acc0, a0, a1);
