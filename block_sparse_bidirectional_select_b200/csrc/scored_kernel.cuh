@@ -28,13 +28,13 @@
 //
 // Capped scores. tanh(u) = u * P(u^2), P by a minimax fit (the coefficients are
 // scaled on the host so that the polynomial takes the raw product and gives
-// log2 units): of degree 2 for |u| <= 0.25 (absolute error 5e-8) and 3 for
-// |u| <= 0.5 (1.3e-7, the rounding of a score of that size). The narrow one
+// log2 units): of degree 2 for |u| <= 0.25 (off by 4e-7 of the score) and 3
+// for |u| <= 0.5 (5.7e-7; a few roundings of a score). The narrow one
 // costs four packed FP32 operations for two scores, one of which replaces the
 // scaling of the plain path; a packed operation takes the FP32 pipe two clocks,
 // which is what a capped pass pays for. A warp whose tile holds a larger score
-// takes 1 - 2 / (1 + e^2u), two MUFU operations, whose absolute error (2^-23) is
-// as good; MUFU is what bounds that path (16 operations a clock and SM, three
+// takes 1 - 2 / (1 + e^2u), two MUFU operations, whose error (2^-23 of the
+// cap) is as good for scores of that size; MUFU is what bounds that path (16 operations a clock and SM, three
 // per score with the softmax's own).
 //
 // Measured, 32 heads of 8192 tokens, d = 128: 1004 us plain (attn_fwd_kernel:

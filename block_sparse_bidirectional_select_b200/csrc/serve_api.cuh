@@ -135,12 +135,15 @@ int launch_scored(const ScoredMaps& t, const ScoredArgs& a, bool cap, int dev, i
 }
 
 // Capped scores in log2 units: y = s * P(s^2) while |s| * scale / cap <= 0.5,
-// with tanh(u) = u * (c0 + c1 u^2 + c2 u^4 + c3 u^6) to 1.3e-7 there, and with
-// u * (n0 + n1 u^2 + n2 u^4) to 5e-8 while it is at most 0.25 (minimax fits).
+// with tanh(u) = u * (c0 + c1 u^2 + c2 u^4 + c3 u^6) to 5.7e-7 of it there, and
+// with u * (n0 + n1 u^2 + n2 u^4) to 4e-7 of it while it is at most 0.25. The
+// fits are minimax in the relative error: a fit of the absolute one is off by
+// 1.4e-6 to 2.3e-6 of a score far below the cap, which a row of few keys shows
+// in its log-sum.
 template <typename Args>
 void cap_coefficients(float scale, float softcap, Args* a) {
-  constexpr double kC[4] = {0.9999976761831301, -0.3332065518031203, 0.1314514529551474, -0.04337247410609953};
-  constexpr double kN[3] = {0.9999986329824756, -0.33315701527853825, 0.12762231570462274};
+  constexpr double kC[4] = {0.9999994765759067, -0.33326466944456906, 0.13191881871914507, -0.044444433804554644};
+  constexpr double kN[3] = {0.999999608340289, -0.3332195994712142, 0.12842442158716916};
   const double u = static_cast<double>(scale) / softcap, cl = softcap * 1.4426950408889634;
   double f = cl * u;
   bool finite = true;

@@ -400,6 +400,31 @@ def test_scored_modified(d, softcap, bias, spread):
     check_scored(q[:, :100], k, v, softcap, slopes_of(4) * 40 if bias else None, q_start=-1000)
 
 
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("softcap", [4000.0, 250.0])
+def test_capped_scores_far_below_the_cap(d, softcap):
+    """A row that sees one key has its score as log-sum. With one product per
+    score, exact in fp32, a score is off by the tanh polynomial's 5.7e-7 and at
+    most six roundings of 2^-24 (coefficients, square, steps, log 2), together
+    below 1e-6; the logarithm adds MUFU's 2^-22 times its argument's exponent
+    (the cache's weights stand at 2^7) and the final sums another 2^-22."""
+    L = 64
+    x = torch.linspace(-100.0, 100.0, L, device="cuda").bfloat16()
+    q = torch.zeros(2, L, d, dtype=torch.bfloat16, device="cuda")
+    q[:, :, 3] = x
+    k = torch.zeros(2, L, d, dtype=torch.bfloat16, device="cuda")
+    k[:, :, 3] = 1.0
+    want = softcap * torch.tanh(x.double() / softcap)
+    tol = 1e-6 * want.abs() + 9 * 2.0 ** -22
+    at = torch.arange(L, device="cuda")
+    ranges = torch.stack([at, at + 1], 1).int().contiguous()
+    _, lse = sp.scored_attn(q, k, k, scale=1.0, softcap=softcap, ranges=ranges)
+    assert ((lse.double() - want).abs() <= tol).all(), float(((lse.double() - want).abs() / tol).max())
+    cache = sp.cache_append(sp.cache_alloc(1, 2, 64, d), k[None, :, :1], k[None, :, :1], i32([0]))
+    _, lse = sp.cache_attn(q[None], cache, i32([1]), scale=1.0, softcap=softcap)
+    assert ((lse.double() - want).abs() <= tol).all(), float(((lse.double() - want).abs() / tol).max())
+
+
 @pytest.mark.parametrize("softcap,bias", [(0.0, False), (30.0, False), (0.0, True)])
 def test_scored_documents_and_prefixes(softcap, bias):
     g = gen(41)
