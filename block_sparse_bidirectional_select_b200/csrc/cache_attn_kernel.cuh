@@ -710,6 +710,11 @@ __global__ void __launch_bounds__(CacheCfg<D, Q>::THREADS, 1)
       if (lane == 0) ptx::mbar_arrive(bar(C::B_JOIN));
       return ptx::mbar_wait_warp(bar(C::B_JOIN), joins++ & 1, abort_flag, a.timeout_ns, kErrTimeout);
     };
+    // Few rows: PV of my last tile before g, in the same buffers, is complete.
+    auto pv_before = [&](int g, int b) -> bool {
+      return !FEW || g < 2 ||
+             ptx::mbar_wait_warp(bar(C::B_PVDONE + b), ((g - 2) >> 1) & 1, abort_flag, a.timeout_ns, kErrTimeout);
+    };
     int cq = 0;      // Q copies so far
     int eq_new = 0;  // the last copy's exponent of my row
     // Q of a part into TMEM Q_{cq&1}, hi and lo. First each row by D/8 threads of
@@ -1024,8 +1029,11 @@ __global__ void __launch_bounds__(CacheCfg<D, Q>::THREADS, 1)
             m = m_new;
             fresh = false;
           } else if (__any_sync(0xffffffffu, m_new > m + 8.0f)) {
-            // every PV before this tile's is complete, and this one's waits for me
-            if (!ptx::mbar_wait_warp(bar(C::B_PVDONE + ((g - 1) & 1)), ((g - 1) >> 1) & 1, abort_flag, a.timeout_ns,
+            // every PV before this tile's is complete, and this one's waits for me.
+            // Few rows: S(g) may be there before PV(g-3) is done, when the bit of
+            // PV(g-1)'s phase still says the one before it; PV(g-2) follows PV(g-3).
+            if (!pv_before(g, b) ||
+                !ptx::mbar_wait_warp(bar(C::B_PVDONE + ((g - 1) & 1)), ((g - 1) >> 1) & 1, abort_flag, a.timeout_ns,
                                      kErrTimeout)) {
               ok = false;
               break;
@@ -1064,8 +1072,7 @@ __global__ void __launch_bounds__(CacheCfg<D, Q>::THREADS, 1)
           ptx::f32x2_split(acc1, b0, b1);
           l += (a0 + b0) + (a1 + b1);
           if constexpr (FEW) {  // the last P of these columns has been read
-            if (g >= 2 && !ptx::mbar_wait_warp(bar(C::B_PVDONE + b), ((g - 2) >> 1) & 1, abort_flag, a.timeout_ns,
-                                               kErrTimeout)) {
+            if (!pv_before(g, b)) {
               ok = false;
               break;
             }
@@ -1073,6 +1080,11 @@ __global__ void __launch_bounds__(CacheCfg<D, Q>::THREADS, 1)
           }
           ptx::tmem_st16x2<N / 2>(lane_base + (b ? C::TM_P1 : C::TM_P0) + copy * (C::COLS / 2), pk);
           ptx::tmem_wait_st();
+        } else if (!pv_before(g, b)) {
+          // a warp without rows keeps the others' pace: two arrivals of it in one
+          // phase of PFULL would let PV begin before a slower warp's P is there
+          ok = false;
+          break;
         }
         ptx::tc_fence_before();
         __syncwarp();

@@ -210,6 +210,27 @@ def test_cache_attn(d, N, Hq, Hkv, B, C, lengths):
     check_cache_attn(randn(g, N, Hq, B, d), c, lengths)
 
 
+@pytest.mark.parametrize("N,Hq,Hkv,B,C,d,softcap,bias", [
+    (28, 48, 16, 16, 512, 64, 20.0, False), (13, 48, 16, 16, 2240, 128, 0.0, False), (10, 48, 16, 16, 1152, 128, 0.0, True),
+    (20, 32, 16, 18, 1216, 64, 0.0, False), (7, 64, 32, 32, 2432, 64, 0.0, False), (13, 64, 32, 32, 1216, 128, 0.0, False),
+    (16, 64, 16, 1, 2048, 64, 20.0, False), (6, 32, 32, 16, 5824, 64, 0.0, False), (26, 32, 32, 1, 1216, 128, 0.0, False),
+    (21, 8, 8, 64, 384, 128, 0.0, False)])
+def test_cache_attn_many_short_parts(N, Hq, Hkv, B, C, d, softcap, bias):
+    """Warps that hold no rows, and rows whose maximum rises while the other
+    half's tiles lag: several calls, bit for bit the same."""
+    g = gen(N * C + B)
+    q = randn(g, N, Hq, B, d, scale=4.0)
+    c = random_cache(g, N, Hkv, C, d)
+    lengths = [C - 37 * n % (C // 2) for n in range(N)]
+    slopes = slopes_of(Hq) if bias else None
+    check_cache_attn(q, c, lengths, softcap, slopes)
+    first = sp.cache_attn(q, c, i32(lengths), softcap=softcap, slopes=slopes)
+    for _ in range(20):
+        again = sp.cache_attn(q, c, i32(lengths), softcap=softcap, slopes=slopes)
+        assert torch.equal(first[0], again[0]) and torch.equal(first[1], again[1])
+    sp.device_check()
+
+
 @pytest.mark.parametrize("softcap,bias,given", [(5.0, False, False), (50.0, False, False), (0.0, True, False),
                                                 (30.0, True, True)])
 def test_cache_attn_modified_scores(softcap, bias, given):
