@@ -63,7 +63,7 @@
 // Measured: 16 single tokens of 32 heads on 8 over 16384 keys (537 MB) 116 us,
 // 4.6 TB/s with set-up, joins and launches, 5.2 TB/s in the steady state; a
 // single token over 8192 keys 17 us, of which the tiles are 4; 64-token blocks of
-// 64 heads over 32768 keys with a bias 162 us. The single tokens are bound by
+// 64 heads over 32768 keys with a bias 162 to 168 us. The single tokens are bound by
 // HBM, the blocks by the softmax chain of a tile.
 #pragma once
 
