@@ -1110,7 +1110,9 @@ __global__ void __launch_bounds__(CacheCfg<D, Q>::THREADS, 1)
 // kMergeRows rows. Thread c looks whether run c holds part of the item; a warp
 // then takes whole rows. `runs`: the CTAs of the attention kernel. Launched as
 // its programmatic dependent: only the part after grid_dep_wait reads its
-// results.
+// results. Every CTA waits before it ends, also one that has nothing to join:
+// what follows on the stream is ordered behind this grid alone, which must not
+// end before the attention kernel's last rows are written.
 constexpr int kMergeRows = 10;
 template <int D>
 __global__ void __launch_bounds__(kCacheMaxCtas) cache_merge_kernel(const __grid_constant__ CacheArgs a, int runs) {
@@ -1125,7 +1127,10 @@ __global__ void __launch_bounds__(kCacheMaxCtas) cache_merge_kernel(const __grid
   const int hk = item / a.RT, rt = item - hk * a.RT;
   const int r0 = blockIdx.z * kMergeRows;
   const int r1 = min(min(128, a.R - rt * 128), r0 + kMergeRows);
-  if (r0 >= r1) return;
+  if (r0 >= r1) {
+    ptx::grid_dep_wait();
+    return;
+  }
   const long grow0 = (static_cast<long>(n) * a.Hkv + hk) * a.R + rt * 128;
   const int nt = cache_tiles(a, cache_len(a, n));
   if (nt == 0) {
@@ -1151,10 +1156,10 @@ __global__ void __launch_bounds__(kCacheMaxCtas) cache_merge_kernel(const __grid
     at += w < warp ? s_count[w] : 0;
     count += s_count[w];
   }
-  if (count == 1) return;  // whole in one run: written there
   if (holds) s_slot[at + __popc(vote & ((1u << lane) - 1u))] = 2 * c + (b0 <= x0 ? 1 : 0);
   __syncthreads();
   ptx::grid_dep_wait();
+  if (count == 1) return;  // whole in one run: written there
   using Vec = typename std::conditional<V == 4, float4, float2>::type;
   constexpr int BATCH = 8;  // slots whose loads are in flight together
   const long slot_stride = static_cast<long>(a.part_rows) * D;
