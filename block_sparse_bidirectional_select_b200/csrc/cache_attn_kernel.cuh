@@ -710,7 +710,8 @@ __global__ void __launch_bounds__(CacheCfg<D, Q>::THREADS, 1)
       if (lane == 0) ptx::mbar_arrive(bar(C::B_JOIN));
       return ptx::mbar_wait_warp(bar(C::B_JOIN), joins++ & 1, abort_flag, a.timeout_ns, kErrTimeout);
     };
-    // Few rows: PV of my last tile before g, in the same buffers, is complete.
+    // Few rows: PV of the last tile before g in the same buffers (of my last one
+    // before it, where g is mine) is complete.
     auto pv_before = [&](int g, int b) -> bool {
       return !FEW || g < 2 ||
              ptx::mbar_wait_warp(bar(C::B_PVDONE + b), ((g - 2) >> 1) & 1, abort_flag, a.timeout_ns, kErrTimeout);
@@ -822,8 +823,11 @@ __global__ void __launch_bounds__(CacheCfg<D, Q>::THREADS, 1)
         break;
       }
       if (have) {
-        // ---- epilogue
-        if (!ptx::mbar_wait_warp(bar(C::B_PVDONE + ((g - 1) & 1)), ((g - 1) >> 1) & 1, abort_flag, a.timeout_ns,
+        // ---- epilogue. PV(g-1) is the part's last. Few rows: a warp whose own
+        // last tile is g-2 knows of no PV after g-4, and the bit of PV(g-1)'s
+        // phase may still be that of PV(g-3): PV(g-2) first, which follows it.
+        if (!pv_before(g, g & 1) ||
+            !ptx::mbar_wait_warp(bar(C::B_PVDONE + ((g - 1) & 1)), ((g - 1) >> 1) & 1, abort_flag, a.timeout_ns,
                                  kErrTimeout)) {
           ok = false;
           break;

@@ -61,3 +61,60 @@ def test_the_return_scan_finds_an_early_return():
     assert returns_before_a_wait("{ if (x) return; grid_dep_wait(); }")
     assert returns_before_a_wait("{ if (x) { grid_dep_wait(); } return; }")
     assert not returns_before_a_wait("{ if (x) { grid_dep_wait(); return; } grid_dep_wait(); if (y) return; }")
+
+
+# ------------------------------------------------------------------ phases of an mbarrier
+
+class Waiter:
+    """What one warp knows about operations that complete in order and arrive
+    alternately on two barriers. A wait for operation n looks at one bit: it
+    can only tell phase n from n - 2, so n - 2 has to be known complete."""
+
+    def __init__(self):
+        self.known = -1
+
+    def wait(self, n):
+        if n >= 0:
+            assert n <= self.known or n - 2 <= self.known, f"the wait for {n} may pass at {n - 2}: known {self.known}"
+            self.known = max(self.known, n)
+
+
+def softmax_waits(parts, hw, next_copy, mended=True):
+    """cache_attn_kernel, few rows: the waits on PV of a softmax warp of parity
+    hw over a run's parts (numbers of tiles), rescaling O at each of its tiles.
+    next_copy: count what it learns where the warps join for the next part's Q."""
+    w, g0 = Waiter(), 0
+    for i, cnt in enumerate(parts):
+        skip = (g0 ^ hw) & 1
+        for jj in range(skip, cnt, 2):
+            g = g0 + jj
+            if jj > skip:           # a rescale
+                w.wait(g - 2)
+                w.wait(g - 1)
+            w.wait(g - 2)           # before P is stored
+        g = g0 + cnt
+        if next_copy and i + 1 < len(parts):
+            w.known = max(w.known, g - 3)   # the join of the next part's copy: tile g - 1's owners waited for g - 3
+        if mended:
+            w.wait(g - 2)
+        w.wait(g - 1)
+        g0 = g
+
+
+PARTS = [[n] for n in range(1, 9)] + [[a, b, c] for a in (1, 2, 3, 4) for b in (1, 2, 5) for c in (1, 3, 4)]
+
+
+@pytest.mark.parametrize("hw", [0, 1])
+def test_cache_attention_waits_tell_their_phase(hw):
+    for parts in PARTS:
+        softmax_waits(parts, hw, next_copy=False)
+    with pytest.raises(AssertionError, match="may pass"):
+        for parts in PARTS:
+            softmax_waits(parts, hw, next_copy=True, mended=False)   # a run's last part has no join before its end
+
+
+def test_cache_attention_epilogue_waits_for_the_tile_before_the_last():
+    body = kernel_body(source("cache_attn_kernel.cuh"), "cache_attn_kernel")
+    at = body.index("if (have) {")
+    assert re.match(r"if \(have\) \{\s*if \(!pv_before\(g, g & 1\) \|\|\s*!ptx::mbar_wait_warp\(bar\(C::B_PVDONE "
+                    r"\+ \(\(g - 1\) & 1\)\)", body[at:])
