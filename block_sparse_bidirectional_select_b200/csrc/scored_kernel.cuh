@@ -71,6 +71,10 @@ struct ScoredCfg {
   static constexpr int BK = 128;
   using A = AttnCfg<D, BK>;
   static constexpr int NST = A::NST;
+  // Split: a slot waits for its own tiles only, every second K and V, so the
+  // use of a stage before must be its own too. A wait can tell a phase from
+  // the one before it, and no order of loads says that another slot's has landed.
+  static constexpr int NST_SPLIT = NST & ~3;
   static constexpr int B_VOK = A::NUM_BARS;           // [NST] V tile cleared of unseen rows
   static constexpr int B_JOIN = B_VOK + NST;          // split: slot 1's sums are in shared memory, 4 warp arrivals
   static constexpr int NUM_BARS = B_JOIN + 1;
@@ -79,6 +83,7 @@ struct ScoredCfg {
   static constexpr int OFF_JOIN = (OFF_MISC + 48 + 15) & ~15;  // split: (max, sum) of slot 1's rows
   static constexpr int SMEM_BYTES = OFF_JOIN + 128 * 8 + 1024;
   static_assert(SMEM_BYTES <= A::SMEM_LIMIT, "shared memory budget");
+  static_assert(NST_SPLIT >= 4, "ring too shallow");
 };
 
 template <int R>
@@ -244,7 +249,7 @@ __global__ void __launch_bounds__(384, 1)
   using S = ScoredCfg<D>;
   using C = typename S::A;
   constexpr int BK = S::BK;
-  constexpr int NST = C::NST;
+  constexpr int NST = SPLIT ? S::NST_SPLIT : S::NST;  // ring stages in use
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~static_cast<uintptr_t>(1023));
@@ -276,7 +281,8 @@ __global__ void __launch_bounds__(384, 1)
     }
     for (int s = 0; s < NST; ++s) {
       ptx::mbar_init(bar(C::B_FULL + s), 1);
-      ptx::mbar_init(bar(C::B_EMPTY + s), a.ranges ? 3 : 2);  // two commits per tile, and warp 11
+      // two arrivals per tile: one of each slot, or (split) both of the tile's own; and warp 11
+      ptx::mbar_init(bar(C::B_EMPTY + s), a.ranges ? 3 : 2);
       ptx::mbar_init(bar(S::B_VOK + s), 1);
     }
     ptx::mbar_init(bar(S::B_JOIN), 4);
@@ -440,12 +446,24 @@ __global__ void __launch_bounds__(384, 1)
         if (lane == 0) ptx::mbar_arrive(bar(C::B_WEMPTY + (np & 1)));
         if (w >= n_pairs) break;
         const ScoredPair pr = scored_pair(a, w, nph);
-        const bool sole = !pr.has1;       // a tile has one slot, which gives both commits
         const int first = split ? s : 0;  // my first tile
         for (int j = 0; j < nj; ++j) {
           const int sk = seq, sv = seq + 1;
           seq += 2;
-          if (split ? (j & 1) != s : (s == 1 && !pr.has1)) continue;
+          if (split && (j & 1) != s) continue;
+          if (s == 1 && !split && !pr.has1) {
+            // no query tile of mine: I keep the ring's pace, so that my next
+            // wait on a stage can tell its phase
+            if (!wait(C::B_FULL + sk % NST, sk / NST) || !wait(C::B_FULL + sv % NST, sv / NST)) {
+              ok = false;
+              break;
+            }
+            if (lane == 0) {
+              ptx::mbar_arrive(bar(C::B_EMPTY + sk % NST));
+              ptx::mbar_arrive(bar(C::B_EMPTY + sv % NST));
+            }
+            continue;
+          }
           if ((j == first && !wait(C::B_QFULL + s, qn++)) || !wait(C::B_FULL + sk % NST, sk / NST)) {
             ok = false;
             break;
@@ -462,7 +480,7 @@ __global__ void __launch_bounds__(384, 1)
           }
           commit(C::B_SFULL + s);
           commit(C::B_EMPTY + sk % NST);
-          if (sole) commit(C::B_EMPTY + sk % NST);
+          if (split) commit(C::B_EMPTY + sk % NST);
           if (j + (split ? 2 : 1) >= nj) commit(C::B_QEMPTY + s);
           // with ranges, the V tile once warp 11 has passed it
           if (!wait(C::B_FULL + sv % NST, sv / NST) || (a.ranges && !wait(S::B_VOK + sv % NST, sv / NST))) {
@@ -487,7 +505,7 @@ __global__ void __launch_bounds__(384, 1)
           if (!ok) break;
           commit(C::B_PVDONE + s);
           commit(C::B_EMPTY + sv % NST);
-          if (sole) commit(C::B_EMPTY + sv % NST);
+          if (split) commit(C::B_EMPTY + sv % NST);
           ++tcnt;
         }
         if (!ok) break;

@@ -3,6 +3,7 @@ GPU: on the source, or on a model of which phases of an mbarrier a warp knows
 to be complete when it waits for the next one."""
 import os
 import re
+import subprocess
 
 import pytest
 
@@ -118,3 +119,64 @@ def test_cache_attention_epilogue_waits_for_the_tile_before_the_last():
     at = body.index("if (have) {")
     assert re.match(r"if \(have\) \{\s*if \(!pv_before\(g, g & 1\) \|\|\s*!ptx::mbar_wait_warp\(bar\(C::B_PVDONE "
                     r"\+ \(\(g - 1\) & 1\)\)", body[at:])
+
+
+# ------------------------------------------------------------------ ring stages of scored_attn
+
+class RingWaiter:
+    """What a warp knows about loads that complete in any order: those that it
+    waited for, and those whose stage was loaded again before one of them (the
+    producer loads in order, and a stage only when its last load was consumed)."""
+
+    def __init__(self, stages):
+        self.stages, self.waited, self.top = stages, set(), -1
+
+    def wait(self, seq):
+        p = seq - self.stages
+        assert p < 0 or p in self.waited or p + self.stages <= self.top, f"the wait for load {seq} may pass at {p}"
+        self.waited.add(seq)
+        self.top = max(self.top, seq)
+
+
+def ring_waits(stages, split, turns, slot, follows=True):
+    """The loads that an issuer of scored_attn_kernel waits for: K_j is load
+    2 j, V_j load 2 j + 1. turns: (tiles, whether slot 1 has a query tile)."""
+    w, seq = RingWaiter(stages), 0
+    for tiles, has1 in turns:
+        for j in range(tiles):
+            if (j & 1) == slot if split else (slot == 0 or has1 or follows):
+                w.wait(seq)
+                w.wait(seq + 1)
+            seq += 2
+
+
+TURNS = [[(n, b) for n in (1, 2, 3, 9)] + [(5, True), (7, False), (4, True)] for b in (False, True)]
+
+
+def test_scored_attention_waits_tell_their_phase(tmp_path):
+    """With the ring sizes of the build, compiled from its headers."""
+    from block_sparse_bidirectional_select_b200.build import CSRC as csrc, nvcc_path
+    src, exe = tmp_path / "ring.cu", tmp_path / "ring"
+    src.write_text('#include <cstdio>\n#include "scored_kernel.cuh"\nusing namespace sparsed;\n'
+                   'int main() { std::printf("%d %d %d %d\\n", ScoredCfg<64>::NST, ScoredCfg<64>::NST_SPLIT, '
+                   'ScoredCfg<128>::NST, ScoredCfg<128>::NST_SPLIT); }\n')
+    subprocess.run([nvcc_path(), "-gencode", "arch=compute_100a,code=sm_100a", "-std=c++17", "-I", csrc, "-o",
+                    str(exe), str(src)], check=True)
+    sizes = [int(x) for x in subprocess.run([str(exe)], check=True, capture_output=True, text=True).stdout.split()]
+    for slot in (0, 1):
+        for ring, ring_split in (sizes[:2], sizes[2:]):
+            ring_waits(ring_split, True, [(40, False)], slot)
+            for turns in TURNS:
+                ring_waits(ring, False, turns, slot)
+
+
+def test_the_ring_model_finds_the_unsafe_forms():
+    with pytest.raises(AssertionError, match="may pass"):
+        ring_waits(5, True, [(8, False)], 0)
+    with pytest.raises(AssertionError, match="may pass"):
+        ring_waits(5, False, [(3, False), (3, True)], 1, follows=False)
+    # the issuers do follow, and the split form has its own ring
+    body = kernel_body(source("scored_kernel.cuh"), "scored_attn_kernel")
+    assert "constexpr int NST = SPLIT ? S::NST_SPLIT : S::NST;" in body
+    skip = body[body.index("if (s == 1 && !split && !pr.has1) {"):]
+    assert skip.index("C::B_FULL + sk % NST") < skip.index("C::B_FULL + sv % NST") < skip.index("continue;")
