@@ -49,8 +49,9 @@ from __future__ import annotations
 
 import ctypes
 import functools
+import inspect
 import math
-from dataclasses import dataclass
+from dataclasses import dataclass, is_dataclass
 
 import torch
 
@@ -78,6 +79,54 @@ def _ptr(t: torch.Tensor | None):
 def _stream(stream=None):
     s = torch.cuda.current_stream() if stream is None else stream
     return ctypes.c_void_p(s.cuda_stream)
+
+
+def _tensors(x):
+    """The tensors in an argument or result: itself, or those of a sequence or dataclass."""
+    if isinstance(x, torch.Tensor):
+        yield x
+    elif isinstance(x, (tuple, list)):
+        for y in x:
+            yield from _tensors(y)
+    elif is_dataclass(x) and not isinstance(x, type):
+        yield from _tensors(list(vars(x).values()))
+
+
+def _streamed(fn):
+    """Runs ``fn`` on its argument ``stream``, where one is given, by making it
+    the current stream of the call: what the call allocates then comes from
+    that stream's memory. A block of the caller's stream could be one that work
+    still pending there is using (a call's workspace is free for the next as
+    soon as the call returns). Arguments and results are recorded on the
+    stream that did not allocate them, so that neither is reused too soon."""
+    at = list(inspect.signature(fn).parameters).index("stream")
+
+    @functools.wraps(fn)
+    def call(*args, **kw):
+        if len(args) > at:
+            stream, args = args[at], (*args[:at], None, *args[at + 1:])
+            if "stream" in kw:
+                return fn(*args, **kw)  # given twice: the TypeError of such a call
+        else:
+            stream = kw.pop("stream", None)
+        if stream is None:
+            return fn(*args, **kw)
+        given = [t for t in _tensors([*args, *kw.values()]) if t.is_cuda]
+        for t in given:
+            if t.device != stream.device:
+                raise ValueError(f"a tensor is on {t.device}, the stream on {stream.device}")
+        caller = torch.cuda.current_stream(stream.device)
+        with torch.cuda.stream(stream):
+            result = fn(*args, **kw)
+        if stream != caller:
+            for t in given:
+                t.record_stream(stream)
+            for t in _tensors(result):
+                if t.is_cuda:
+                    t.record_stream(caller)
+        return result
+
+    return call
 
 
 def _check_qkv(q, k, v):
@@ -726,19 +775,11 @@ def _check_flat(name, t, dtype, shape):
                          f"got {t.dtype} {tuple(t.shape)}")
 
 
-def _launch(name, dev, stream, keep, args):
-    """Calls the entry point with `dev` current, on its current stream or on
-    `stream`. For a stream given by the caller, the tensors in `keep` (which
-    may be freed before its work is done) are recorded on it."""
+def _launch(name, dev, args):
+    """Calls the entry point with `dev` current, on its current stream."""
     fn = getattr(_lib.load(), name)
     index = dev.index
-    if stream is None:
-        handle = _raw_stream(index)
-    else:
-        handle = stream.cuda_stream
-        for t in keep:
-            if t is not None:
-                t.record_stream(stream)
+    handle = _raw_stream(index)
     if index == torch.cuda.current_device():
         rc = fn(*args, handle)
     else:
@@ -775,6 +816,7 @@ def _sections(sections):
 _default_scale = functools.lru_cache(maxsize=16)(default_scale)
 
 
+@_streamed
 def rope_axes(x, positions, sections, theta=10000.0, interleaved=False, shared_ladder=False, inverse=False,
               out=None, stream=None):
     """Rotary positions with several axes. x [H, L, d] bf16 (any strides, the
@@ -800,7 +842,7 @@ def rope_axes(x, positions, sections, theta=10000.0, interleaved=False, shared_l
         out_shape, ys = _strided("out", out, 3)
         if out_shape != shape:
             raise ValueError(f"out must be shaped {tuple(shape)}, got {tuple(out_shape)}")
-    _launch("sparsed_rope_axes", dev, stream, (x, positions, out),
+    _launch("sparsed_rope_axes", dev,
             (x.data_ptr(), xs[0], xs[1], positions.data_ptr(), axes, ctypes.addressof(pairs), H, L, d, theta,
              int(interleaved), int(shared_ladder), int(inverse), out.data_ptr(), ys[0], ys[1]))
     return out
@@ -846,6 +888,7 @@ def _check_cache(cache):
     return N, H, C, d, dev
 
 
+@_streamed
 def cache_append(cache: Cache8, k, v, start, count=None, stream=None) -> Cache8:
     """Write k, v [N, Hkv, B, d] bf16 (any strides, the last dimension
     contiguous) into the cache: the first count[n] tokens (default: all B) of
@@ -861,8 +904,7 @@ def cache_append(cache: Cache8, k, v, start, count=None, stream=None) -> Cache8:
     if count is not None:
         _check_flat("count", count, torch.int32, (N,))
     _device_of(cache.k8, k=k, v=v, start=start, count=count)
-    _launch("sparsed_cache_append", dev, stream,
-            (k, v, start, count, cache.k8, cache.v8, cache.k_scale, cache.v_scale),
+    _launch("sparsed_cache_append", dev,
             (k.data_ptr(), *ks, v.data_ptr(), *vs, N, H, B, C, d, start.data_ptr(), _data(count),
              cache.k8.data_ptr(), cache.v8.data_ptr(), cache.k_scale.data_ptr(), cache.v_scale.data_ptr()))
     return cache
@@ -876,6 +918,7 @@ def cache_attn_workspace_bytes(N: int, Hq: int, Hkv: int, B: int, d: int) -> int
     return n.value
 
 
+@_streamed
 def cache_attn(q, cache: Cache8, lengths, scale=None, softcap=0.0, slopes=None, q_start=None, out=None, lse=None,
                workspace=None, stream=None):
     """Attention of q [N, Hq, B, d] bf16 (one token or a block per sequence)
@@ -900,8 +943,7 @@ def cache_attn(q, cache: Cache8, lengths, scale=None, softcap=0.0, slopes=None, 
     lse = _out_like("lse", lse, q, shape[:3], torch.float32)
     if workspace is None:
         workspace = q.new_empty(cache_attn_workspace_bytes(N, Hq, Hkv, B, d), dtype=torch.uint8)
-    _launch("sparsed_cache_attn", dev, stream,
-            (q, cache.k8, cache.v8, cache.k_scale, cache.v_scale, lengths, q_start, slopes, out, lse, workspace),
+    _launch("sparsed_cache_attn", dev,
             (q.data_ptr(), *qs, cache.k8.data_ptr(), cache.v8.data_ptr(), cache.k_scale.data_ptr(),
              cache.v_scale.data_ptr(), N, Hq, Hkv, B, C, d, lengths.data_ptr(), _data(q_start),
              _default_scale(d) if scale is None else scale, softcap, _data(slopes), out.data_ptr(), lse.data_ptr(),
@@ -909,6 +951,7 @@ def cache_attn(q, cache: Cache8, lengths, scale=None, softcap=0.0, slopes=None, 
     return out, lse
 
 
+@_streamed
 def document_ranges(starts, L: int, prefix=None, stream=None):
     """Visible keys of packed documents for scored_attn: ranges [L, 2] int32.
     starts [n + 1] int32 (device, ascending): document i holds tokens
@@ -923,7 +966,7 @@ def document_ranges(starts, L: int, prefix=None, stream=None):
         _check_flat("prefix", prefix, torch.int32, (n,))
     dev = _device_of(starts, prefix=prefix)
     ranges = starts.new_empty((L, 2))
-    _launch("sparsed_document_ranges", dev, stream, (starts, prefix, ranges),
+    _launch("sparsed_document_ranges", dev,
             (starts.data_ptr(), _data(prefix), n, L, ranges.data_ptr()))
     return ranges
 
@@ -936,6 +979,7 @@ def scored_attn_workspace_bytes(Hq: int, Lq: int) -> int:
     return n.value
 
 
+@_streamed
 def scored_attn(q, k, v, scale=None, softcap=0.0, slopes=None, ranges=None, q_start=0, out=None, lse=None,
                 workspace=None, stream=None):
     """Dense attention with modified scores: q [Hq, Lq, d], k, v [Hkv, Lk, d]
@@ -960,7 +1004,7 @@ def scored_attn(q, k, v, scale=None, softcap=0.0, slopes=None, ranges=None, q_st
     lse = _out_like("lse", lse, q, shape[:2], torch.float32)
     if workspace is None:
         workspace = q.new_empty(scored_attn_workspace_bytes(Hq, Lq), dtype=torch.uint8)
-    _launch("sparsed_scored_attn", dev, stream, (q, k, v, slopes, ranges, out, lse, workspace),
+    _launch("sparsed_scored_attn", dev,
             (q.data_ptr(), *qs, k.data_ptr(), *ks, v.data_ptr(), *vs, Hq, Hkv, Lq, Lk, d,
              _default_scale(d) if scale is None else scale, softcap, _data(slopes), q_start, _data(ranges),
              out.data_ptr(), lse.data_ptr(), workspace.data_ptr(), workspace.numel()))

@@ -63,3 +63,48 @@ def test_scored_odd_query_tiles(d):
         again = sp.scored_attn(q, k, v)
         assert torch.equal(first[0], again[0]) and torch.equal(first[1], again[1])
     sp.device_check()
+
+
+def test_calls_back_to_back_on_two_streams():
+    """A call on the current stream and one with ``stream=``, at once and with buffers of the library's: the second
+    one's do not come from memory that the first is still using. Nothing synchronises in between."""
+    g = gen(64)
+    c = random_cache(g, 4, 4, 16384, 128)
+    n = i32([16384, 9000, 12345, 16000])
+    q1, q2 = randn(g, 4, 16, 1, 128), randn(g, 4, 16, 1, 128)
+    want1, want2 = sp.cache_attn(q1, c, n), sp.cache_attn(q2, c, n)
+    sq1, sq2, k, v = (randn(g, h, 3000, 64) for h in (160, 160, 8, 8))
+    swant1, swant2 = sp.scored_attn(sq1, k, v), sp.scored_attn(sq2, k, v)
+    x, pos = randn(g, 16, 4000, 128), i32([list(range(4000))])
+    rwant = sp.rope_axes(x, pos, (64,))
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    for _ in range(10):
+        got1, got2 = sp.cache_attn(q1, c, n), sp.cache_attn(q2, c, n, stream=s)
+        sgot1, sgot2 = sp.scored_attn(sq1, k, v), sp.scored_attn(sq2, k, v, stream=s)
+        rgot = sp.rope_axes(x, pos, (64,), stream=s)
+        torch.cuda.current_stream().wait_stream(s)
+        for got, want in zip((*got1, *got2, *sgot1, *sgot2, rgot), (*want1, *want2, *swant1, *swant2, rwant)):
+            assert torch.equal(got, want)
+        del got1, got2, sgot1, sgot2, rgot, got, want
+    sp.device_check()
+
+
+def test_calls_with_a_stream_of_the_graph():
+    """A captured call that is given the capturing stream, and one that forks to another."""
+    g = gen(65)
+    q, k, v = randn(g, 4, 300, 64), randn(g, 2, 300, 64), randn(g, 2, 300, 64)
+    want = sp.scored_attn(q, k, v)
+    s, side = torch.cuda.Stream(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=s):
+        a = sp.scored_attn(q, k, v, stream=s)
+        side.wait_stream(s)
+        b = sp.scored_attn(q, k, v, stream=side)
+        s.wait_stream(side)
+    for _ in range(3):
+        a[0].zero_(), b[0].zero_()
+        graph.replay()
+        assert torch.equal(a[0], want[0]) and torch.equal(b[0], want[0]) and torch.equal(b[1], want[1])
+    sp.device_check()
