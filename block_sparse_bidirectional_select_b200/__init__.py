@@ -204,6 +204,7 @@ def _workspace(q, bq, bk, workspace):
     return workspace
 
 
+@_streamed
 def dense_attn(q, k, v, scale=None, bq=128, bk=128, out=None, lse=None, stream=None):
     """Dense bidirectional attention: returns (o [H,L,d] bf16, lse [H,L] fp32)."""
     H, L, d = _check_qkv(q, k, v)
@@ -225,6 +226,7 @@ class Pattern:
     head_k: torch.Tensor       # [H] int32
 
 
+@_streamed
 def select_pattern(q, k, v, keep=0.1, budget="uniform", scale=None, bq=128, bk=128, kv_stride=None,
                    return_mass=False, workspace=None, stream=None) -> Pattern:
     """Full-attention pass plus block-sparse pattern selection."""
@@ -249,6 +251,7 @@ def select_pattern(q, k, v, keep=0.1, budget="uniform", scale=None, bq=128, bk=1
     return Pattern(out, lse, kv_idx, kv_count, mass, head_k)
 
 
+@_streamed
 def block_sparse_attn(q, k, v, kv_idx, kv_count, scale=None, bq=128, bk=128, out=None, lse=None,
                       stream=None):
     """Block-sparse attention over a cached pattern: returns (o, lse)."""
@@ -281,6 +284,7 @@ class RunResult:
 DRIFT_AMPLITUDE = 2.0 ** -6
 
 
+@_streamed
 def drift_queries(q, seed: int, t: int, amplitude: float = DRIFT_AMPLITUDE, out=None, stream=None):
     """The queries of denoising step t (sparsed_drift_queries): a seeded
     perturbation of q, the same bits on any machine."""
@@ -293,6 +297,7 @@ def drift_queries(q, seed: int, t: int, amplitude: float = DRIFT_AMPLITUDE, out=
     return out
 
 
+@_streamed
 def run_steps(q, k, v, T, warmup_frac=0.2, keep=0.1, budget="uniform", refresh_every=0, scale=None,
               bq=128, bk=128, start_step=0, pattern=None, time_steps=False, out=None, lse=None,
               workspace=None, stream=None, end_step=None, drift_seed=None,
@@ -373,6 +378,7 @@ class ColumnPattern:
     col_mass: torch.Tensor | None   # [H, L] fp32
 
 
+@_streamed
 def select_columns(q, k, v, keep=0.1, scale=None, bq=128, bk=128, return_mass=False, workspace=None,
                    stream=None) -> ColumnPattern:
     """Full-attention pass plus per-head column selection (column mass, top-k)."""
@@ -390,6 +396,7 @@ def select_columns(q, k, v, keep=0.1, scale=None, bq=128, bk=128, return_mass=Fa
     return ColumnPattern(out, lse, cols, mass)
 
 
+@_streamed
 def column_sparse_attn(q, k, v, cols, scale=None, bq=128, bk=128, out=None, lse=None, workspace=None,
                        stream=None):
     """Attention of every query over its head's kept columns: returns (o, lse)."""
@@ -408,6 +415,7 @@ def column_sparse_attn(q, k, v, cols, scale=None, bq=128, bk=128, out=None, lse=
     return out, lse
 
 
+@_streamed
 def run_steps_columns(q, k, v, T, warmup_frac=0.2, keep=0.1, refresh_every=0, scale=None, bq=128, bk=128,
                       start_step=0, cols=None, time_steps=False, out=None, lse=None, workspace=None,
                       stream=None) -> RunResult:
@@ -434,6 +442,7 @@ def run_steps_columns(q, k, v, T, warmup_frac=0.2, keep=0.1, refresh_every=0, sc
 
 # ---------------------------------------------------------------- head-sharded selection
 
+@_streamed
 def select_head_entropy(q, k, v, scale=None, bq=128, bk=128, workspace=None, stream=None, out=None, lse=None):
     """Full pass, block mass and the mean row entropy of every head:
     returns (o, lse, head_entropy [H] fp64 on the device, workspace). The
@@ -461,6 +470,7 @@ def entropy_budget(head_entropy, nkb: int, keep: float) -> list[int]:
     return list(dst[:H])
 
 
+@_streamed
 def select_with_head_k(H, L, head_k, workspace, bq=128, bk=128, stream=None):
     """Top-k per (head, query block) with given k_h over the block mass a
     preceding select_head_entropy left in ``workspace``: (kv_idx, kv_count)."""
@@ -490,6 +500,7 @@ def gather_head_entropies(ent, group=None):
     return torch.cat([t.cpu() for t in parts]), dist.get_rank(group)
 
 
+@_streamed
 def select_pattern_sharded(q, k, v, keep=0.1, group=None, scale=None, bq=128, bk=128, workspace=None,
                            stream=None, out=None, lse=None, gather=None) -> Pattern:
     """Entropy-budget pattern selection for this rank's heads of a layer whose
@@ -579,6 +590,7 @@ def _block_state(q, P, n_sel, scale, bq, bk, splits, workspace):
                       workspace)
 
 
+@_streamed
 def losa_init(q, k, v, k_pre, v_pre, n_sel=2, scale=None, bq=64, bk=64, splits=None, return_mass=False,
               workspace=None, stream=None):
     """First denoising step of a block: dense prefix attention of every token
@@ -600,6 +612,7 @@ def losa_init(q, k, v, k_pre, v_pre, n_sel=2, scale=None, bq=64, bk=64, splits=N
     return (out, lse, st, mass) if return_mass else (out, lse, st)
 
 
+@_streamed
 def losa_step(q, k, v, q_prev, k_pre, v_pre, state: BlockState, tau: float, return_union=False,
               stream=None) -> LosaStep:
     """A later step of the block: active tokens by query MSE against q_prev,
@@ -625,6 +638,7 @@ def losa_step(q, k, v, q_prev, k_pre, v_pre, state: BlockState, tau: float, retu
     return LosaStep(out, lse, active, ucount, uidx)
 
 
+@_streamed
 def losa_block(qs, ks, vs, k_pre, v_pre, n_sel=2, tau=0.01, scale=None, bq=64, bk=64, splits=None, out=None,
                lse=None, workspace=None, stream=None) -> LosaBlock:
     """All T steps of one block (qs, ks, vs: [T, H, B, d] bf16): the first
@@ -664,6 +678,7 @@ _EXCHANGE_FN = ctypes.CFUNCTYPE(ctypes.c_int, ctypes.POINTER(ctypes.c_double), c
                                 ctypes.POINTER(ctypes.c_double), ctypes.c_int, ctypes.c_void_p)
 
 
+@_streamed
 def run_steps_sharded(q, k, v, T, warmup_frac=0.2, keep=0.1, budget="entropy", refresh_every=0, group=None,
                       scale=None, bq=128, bk=128, out=None, lse=None, workspace=None, stream=None,
                       gather=None, rank=None, world=None) -> RunResult:

@@ -1,6 +1,7 @@
 """The argument ``stream`` of the binding, without a GPU: a call given a stream
 makes it current before it allocates or launches anything."""
 import contextlib
+import inspect
 
 import pytest
 import torch
@@ -69,6 +70,60 @@ def test_a_given_stream_is_current_for_the_whole_call(seen, name):
     del seen[:]
     call()
     assert seen and all(where is None for _, where in seen), seen
+
+
+def loop_calls():
+    x = torch.zeros(2, 128, 64, dtype=torch.bfloat16)
+    idx, count, ws = (torch.zeros(*s, dtype=torch.int32) for s in ((2, 1, 1), (2, 1), (64,)))
+    state = sp.BlockState(x, idx[..., 0].float(), idx, 0.1, 64, 64, 1, ws)
+    return {
+        "dense_attn": lambda **kw: sp.dense_attn(x, x, x, **kw),
+        "select_pattern": lambda **kw: sp.select_pattern(x, x, x, **kw),
+        "block_sparse_attn": lambda **kw: sp.block_sparse_attn(x, x, x, idx, count, **kw),
+        "drift_queries": lambda **kw: sp.drift_queries(x, 1, 1, **kw),
+        "run_steps": lambda **kw: sp.run_steps(x, x, x, 2, **kw),
+        "select_columns": lambda **kw: sp.select_columns(x, x, x, **kw),
+        "column_sparse_attn": lambda **kw: sp.column_sparse_attn(x, x, x, idx[:, 0], **kw),
+        "run_steps_columns": lambda **kw: sp.run_steps_columns(x, x, x, 2, **kw),
+        "select_head_entropy": lambda **kw: sp.select_head_entropy(x, x, x, **kw),
+        "select_with_head_k": lambda **kw: sp.select_with_head_k(2, 128, [1, 1], ws, **kw),
+        "select_pattern_sharded": lambda **kw: sp.select_pattern_sharded(x, x, x, **kw),
+        "losa_init": lambda **kw: sp.losa_init(x, x, x, x, x, splits=1, **kw),
+        "losa_step": lambda **kw: sp.losa_step(x, x, x, x, x, x, state, 0.1, **kw),
+        "run_steps_sharded": lambda **kw: sp.run_steps_sharded(x, x, x, 2, **kw),
+    }
+
+
+@pytest.mark.parametrize("name", list(loop_calls()))
+def test_a_given_stream_is_current_for_the_older_calls_too(seen, monkeypatch, name):
+    class Library:
+        def __getattr__(self, entry):
+            def run(*args):
+                seen.append((entry, torch.cuda.current_stream()))
+                return 0
+            return run
+
+    call = loop_calls()[name]
+    base, stream = FakeStream(), FakeStream()
+    stream.device = torch.device("cpu")   # where this test's tensors are
+    inner = torch.cuda.current_stream
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda device=None: inner() or base)
+    monkeypatch.setattr(sp._lib, "load", lambda *a: Library())
+    monkeypatch.setattr(sp, "_check_qkv", lambda q, k, v: q.shape)
+    monkeypatch.setattr(sp, "_check_prefix", lambda k, v, H, d, dev: k.shape[1])
+    monkeypatch.setattr(torch.Tensor, "is_cuda", property(lambda t: True))
+    del seen[:]
+    call(stream=stream)
+    work = [(what, where) for what, where in seen if not what.endswith(("_bytes", "_keep", "_splits", "entropy_budget"))]
+    assert any(what.startswith("sparsed_") for what, _ in work)
+    assert all(where is stream for _, where in work), work
+
+
+def test_every_call_with_a_stream_goes_through_it():
+    for name in set(sp.__all__) - {"device_check"}:   # which allocates nothing
+        fn = getattr(sp, name)
+        if inspect.isfunction(fn) and "stream" in inspect.signature(fn).parameters:
+            assert hasattr(fn, "__wrapped__"), name
 
 
 def test_results_and_arguments_are_recorded_on_the_other_stream(seen, monkeypatch):
