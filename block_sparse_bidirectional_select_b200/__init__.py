@@ -818,6 +818,15 @@ def _out_like(name, out, like, shape, dtype):
     return out
 
 
+def _check_workspace(workspace):
+    """Bytes of a workspace given by the caller. Its memory is taken as one
+    piece from its first element on, so that views with gaps or repeated
+    elements, whose size says nothing about it, are refused."""
+    if not workspace.is_contiguous():
+        raise ValueError("workspace must be contiguous")
+    return workspace.numel() * workspace.element_size()
+
+
 def _data(t):
     return None if t is None else t.data_ptr()
 
@@ -958,11 +967,12 @@ def cache_attn(q, cache: Cache8, lengths, scale=None, softcap=0.0, slopes=None, 
     lse = _out_like("lse", lse, q, shape[:3], torch.float32)
     if workspace is None:
         workspace = q.new_empty(cache_attn_workspace_bytes(N, Hq, Hkv, B, d), dtype=torch.uint8)
+    room = _check_workspace(workspace)
     _launch("sparsed_cache_attn", dev,
             (q.data_ptr(), *qs, cache.k8.data_ptr(), cache.v8.data_ptr(), cache.k_scale.data_ptr(),
              cache.v_scale.data_ptr(), N, Hq, Hkv, B, C, d, lengths.data_ptr(), _data(q_start),
              _default_scale(d) if scale is None else scale, softcap, _data(slopes), out.data_ptr(), lse.data_ptr(),
-             workspace.data_ptr(), workspace.numel()))
+             workspace.data_ptr(), room))
     return out, lse
 
 
@@ -1019,8 +1029,9 @@ def scored_attn(q, k, v, scale=None, softcap=0.0, slopes=None, ranges=None, q_st
     lse = _out_like("lse", lse, q, shape[:2], torch.float32)
     if workspace is None:
         workspace = q.new_empty(scored_attn_workspace_bytes(Hq, Lq), dtype=torch.uint8)
+    room = _check_workspace(workspace)
     _launch("sparsed_scored_attn", dev,
             (q.data_ptr(), *qs, k.data_ptr(), *ks, v.data_ptr(), *vs, Hq, Hkv, Lq, Lk, d,
              _default_scale(d) if scale is None else scale, softcap, _data(slopes), q_start, _data(ranges),
-             out.data_ptr(), lse.data_ptr(), workspace.data_ptr(), workspace.numel()))
+             out.data_ptr(), lse.data_ptr(), workspace.data_ptr(), room))
     return out, lse
