@@ -662,6 +662,11 @@ __global__ void __launch_bounds__(384, 1)
         bool raw_args = true, narrow = false;
         float mx;
         if constexpr (CAP) {
+          if (masked) {  // keys out of the row's range have no say in the path taken
+#pragma unroll
+            for (int c = 0; c < BK; ++c)
+              if (c0 + c < rg.x || c0 + c >= rg.y) s[c] = 0.f;
+          }
           const float top = row_max(s), low = row_min(s);
           const float far = fmaxf(top, -low);
           const bool wide = __any_sync(0xffffffffu, far > a.cap_fast);
