@@ -1009,7 +1009,10 @@ __global__ void __launch_bounds__(CacheCfg<D, Q>::THREADS, 1)
             }
             if (__any_sync(0xffffffffu, fmaxf(row_max(s), -row_min(s)) > a.cap_fast)) {
 #pragma unroll
-              for (int c = 0; c < N; ++c) y[c] = a.cap_log2 * tanh_wide(s[c] * a.cap_in);
+              for (int c = 0; c < N; ++c) {  // for large scores only: it is off by 2^-22 of the cap
+                const float wide = a.cap_log2 * tanh_wide(s[c] * a.cap_in);
+                y[c] = select_f32(fabsf(s[c]) > a.cap_fast, wide, y[c]);
+              }
             }
 #pragma unroll
             for (int c = 0; c < N; ++c) s[c] = y[c];

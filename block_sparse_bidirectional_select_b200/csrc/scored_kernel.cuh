@@ -33,9 +33,10 @@
 // costs four packed FP32 operations for two scores, one of which replaces the
 // scaling of the plain path; a packed operation takes the FP32 pipe two clocks,
 // which is what a capped pass pays for. A warp whose tile holds a larger score
-// takes 1 - 2 / (1 + e^2u), two MUFU operations, whose error (2^-23 of the
-// cap) is as good for scores of that size; MUFU is what bounds that path (16 operations a clock and SM, three
-// per score with the softmax's own).
+// takes 1 - 2 / (1 + e^2u), two MUFU operations, off by 2^-22 of the cap: as
+// good as the polynomial for scores of that size, and with a cap above 64 kept
+// for those alone (kCapFine). MUFU is what bounds that path (16 operations a
+// clock and SM, three per score with the softmax's own).
 //
 // Measured, 32 heads of 8192 tokens, d = 128: 1004 us plain (attn_fwd_kernel:
 // 995), 1005 with a bias, 1280 capped, 1460 capped and biased. What bounds them
@@ -95,13 +96,38 @@ __device__ __forceinline__ void setmaxnreg_dec() {
   asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(R) : "memory");
 }
 
-// tanh(u) for any u: 1 - 2 / (1 + 2^(2 u log2 e)); saturates to +-1.
+// tanh(u) = u * (c0 + c1 u^2 + c2 u^4 + c3 u^6) while |u| <= 0.5, off by 5.7e-7 of it.
+constexpr double kTanhPoly[4] = {0.9999994765759067, -0.33326466944456906, 0.13191881871914507, -0.044444433804554644};
+
+// tanh(u) for |u| > 0.5: 1 - 2 / (1 + 2^(2 u log2 e)); saturates to +-1.
 __device__ __forceinline__ float tanh_wide(float u) {
   const float e = ptx::ex2(u * 2.885390081777926815f);
   float r;
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.0f + e));
   return fmaf(-2.0f, r, 1.0f);
 }
+// c ? x : y without a branch around x.
+__device__ __forceinline__ float select_f32(bool c, float x, float y) {
+  float r;
+  asm("{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %3, 0;\n\tselp.f32 %0, %1, %2, p;\n\t}"
+      : "=f"(r) : "f"(x), "f"(y), "r"(static_cast<uint32_t>(c)));
+  return r;
+}
+// tanh(u) for any u, off by 2^-20 of itself at most; the wide form is off by
+// 2^-22 (of 1), which a small u shows once a cap multiplies it. In single
+// operations on constants: packed ones on registers spill.
+__device__ __forceinline__ float tanh_any(float u) {
+  constexpr float c0 = static_cast<float>(kTanhPoly[0]), c1 = static_cast<float>(kTanhPoly[1]),
+                  c2 = static_cast<float>(kTanhPoly[2]), c3 = static_cast<float>(kTanhPoly[3]);
+  const float w = u * u;
+  const float p = u * fmaf(fmaf(fmaf(c3, w, c2), w, c1), w, c0);
+  return select_f32(fabsf(u) > 0.5f, tanh_wide(u), p);
+}
+// Up to this cap (64, in log2 units) the wide form serves every score of a warp
+// that has a large one: it is off by 2^-16 there, a 128th of a weight's
+// rounding. With tanh_any 32 heads of 8192 tokens, cap 50, scores of deviation 5
+// and 8, take 1612 and 2848 us instead of 1543 and 2721 (with a bias 2753 instead of 2449).
+constexpr float kCapFine = 64.0f * 1.44269504088896340736f;
 
 __device__ __forceinline__ uint64_t mul_f32x2(uint64_t a, uint64_t b) {
   uint64_t d;
@@ -678,8 +704,15 @@ __global__ void __launch_bounds__(384, 1)
             ptx::f32x2_split(mul_f32x2(v, cap_poly(v, cap)), y0, y1);
             mx = y0;  // the polynomials rise with s and agree to their error
           } else if (wide) {
+            // small scores beside the large ones keep the polynomial, unless the
+            // cap is so low that the wide form's 2^-22 of it is as good
+            if (a.cap_log2 > kCapFine) {
 #pragma unroll
-            for (int c = 0; c < BK; ++c) s[c] = a.cap_log2 * tanh_wide(s[c] * a.cap_in);
+              for (int c = 0; c < BK; ++c) s[c] = a.cap_log2 * tanh_any(s[c] * a.cap_in);
+            } else {
+#pragma unroll
+              for (int c = 0; c < BK; ++c) s[c] = a.cap_log2 * tanh_wide(s[c] * a.cap_in);
+            }
             if constexpr (BIAS) scale_and_bias(s, [&](uint64_t) { return one2; }, slope2, at, c0);
           } else if constexpr (BIAS) {
             if (narrow) scale_and_bias(s, [&](uint64_t v) { return cap_poly_narrow(v, cap_n); }, slope2, at, c0);

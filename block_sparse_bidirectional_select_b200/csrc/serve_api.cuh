@@ -142,7 +142,7 @@ int launch_scored(const ScoredMaps& t, const ScoredArgs& a, bool cap, int dev, i
 // in its log-sum.
 template <typename Args>
 void cap_coefficients(float scale, float softcap, Args* a) {
-  constexpr double kC[4] = {0.9999994765759067, -0.33326466944456906, 0.13191881871914507, -0.044444433804554644};
+  constexpr const double (&kC)[4] = kTanhPoly;
   constexpr double kN[3] = {0.999999608340289, -0.3332195994712142, 0.12842442158716916};
   const double u = static_cast<double>(scale) / softcap, cl = softcap * 1.4426950408889634;
   double f = cl * u;

@@ -32,3 +32,39 @@ def test_capped_scores_and_padding(H, bias, what):
     got = sp.scored_attn(q, k, v, softcap=30.0, slopes=slopes, ranges=ranges)
     assert torch.equal(want[0], got[0]) and torch.equal(want[1], got[1])
     sp.device_check()
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("softcap", [4000.0, 250.0, 50.0])
+def test_small_scores_beside_scores_near_the_cap(d, softcap):
+    """A row that sees one key has its score as log-sum (one product, exact in
+    fp32). Even rows stay below cap / 40, odd ones lie between 0.6 and 0.9 of
+    the cap and are in the same warps. The wide form 1 - 2 / (1 + e), e = e^2u:
+    MUFU's 2^-22 and the rounded argument leave e off by 2^-21 of itself,
+    1 / (1 + e) <= 1 by 2^-21 / 4 and the reciprocal's 2^-23, its double at most 1:
+    together 2^-21.4 of the cap. Large scores are right to 2^-20 of the cap,
+    small ones to the polynomial's 1e-6 of themselves, or to 2^-21 of a cap of
+    at most 64, whose warps take the wide form for all; the log-sum adds 9 * 2^-22
+    (as in the test of scores that are small throughout)."""
+    L = 64
+    g = gen(72)
+    small = (torch.rand(L, generator=g) * 2 - 1) * softcap / 40
+    large = (torch.rand(L, generator=g) * 0.3 + 0.6) * softcap * (1 - 2 * (torch.arange(L) // 2 % 2))
+    odd = torch.arange(L) % 2 == 1
+    x = torch.where(odd, large, small).bfloat16().cuda()
+    q = torch.zeros(2, L, d, dtype=torch.bfloat16, device="cuda")
+    q[:, :, 3] = x
+    k = torch.zeros(2, L, d, dtype=torch.bfloat16, device="cuda")
+    k[:, :, 3] = 1.0
+    want = softcap * torch.tanh(x.double() / softcap)
+    tol = torch.where(odd.cuda(), 2.0 ** -20 * softcap, 1e-6 * want.abs()) + 9 * 2.0 ** -22
+    if softcap <= 64:
+        tol = tol + 2.0 ** -21 * softcap
+    at = torch.arange(L, device="cuda")
+    ranges = torch.stack([at, at + 1], 1).int().contiguous()
+    cache = sp.cache_append(sp.cache_alloc(1, 2, 64, d), k[None, :, :1], k[None, :, :1], i32([0]))
+    for zero in (None, torch.zeros(2, device="cuda")):
+        _, lse = sp.scored_attn(q, k, k, scale=1.0, softcap=softcap, ranges=ranges, slopes=zero)
+        assert ((lse.double() - want).abs() <= tol).all(), float(((lse.double() - want).abs() / tol).max())
+        _, lse = sp.cache_attn(q[None], cache, i32([1]), scale=1.0, softcap=softcap, slopes=zero)
+        assert ((lse.double() - want).abs() <= tol).all(), float(((lse.double() - want).abs() / tol).max())
