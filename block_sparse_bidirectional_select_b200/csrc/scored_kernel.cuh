@@ -35,11 +35,11 @@
 // which is what a capped pass pays for. A warp whose tile holds a larger score
 // takes 1 - 2 / (1 + e^2u), two MUFU operations, off by 2^-22 of the cap: as
 // good as the polynomial for scores of that size, and with a cap above 64 kept
-// for those alone (kCapFine). MUFU is what bounds that path (16 operations a
+// for those alone (kCapHigh). MUFU is what bounds that path (16 operations a
 // clock and SM, three per score with the softmax's own).
 //
-// Measured, 32 heads of 8192 tokens, d = 128: 1004 us plain (attn_fwd_kernel:
-// 995), 1005 with a bias, 1280 capped, 1460 capped and biased. What bounds them
+// Measured, 32 heads of 8192 tokens, d = 128: 1003 us plain (attn_fwd_kernel:
+// 995), 1010 with a bias, 1315 capped, 1505 capped and biased. What bounds them
 // is a slot's chain (S and P share columns, so S waits for PV) and the power cap.
 #pragma once
 
@@ -123,11 +123,14 @@ __device__ __forceinline__ float tanh_any(float u) {
   const float p = u * fmaf(fmaf(fmaf(c3, w, c2), w, c1), w, c0);
   return select_f32(fabsf(u) > 0.5f, tanh_wide(u), p);
 }
-// Up to this cap (64, in log2 units) the wide form serves every score of a warp
-// that has a large one: it is off by 2^-16 there, a 128th of a weight's
-// rounding. With tanh_any 32 heads of 8192 tokens, cap 50, scores of deviation 5
-// and 8, take 1612 and 2848 us instead of 1543 and 2721 (with a bias 2753 instead of 2449).
-constexpr float kCapFine = 64.0f * 1.44269504088896340736f;
+// How the kernel caps its scores: not at all, or by a cap of up to 64 or above.
+// With a low cap the wide form serves every score of a warp that has a large
+// one: it is off by 2^-16 at most, a 128th of a weight's rounding. 32 heads of
+// 8192 tokens, cap 50, scores of deviation 8 take 2640 us with it, 2800 with
+// tanh_any. A choice inside one kernel costs small scores 4% (1300 to 1355 us),
+// so it is the kernel's.
+constexpr int kCapNone = 0, kCapLow = 1, kCapHigh = 2;
+constexpr float kCapLowMost = 64.0f;
 
 __device__ __forceinline__ uint64_t mul_f32x2(uint64_t a, uint64_t b) {
   uint64_t d;
@@ -268,7 +271,15 @@ __device__ __forceinline__ int2 scored_range(const ScoredArgs& a, int r, bool ou
   return v;
 }
 
-template <int D, bool CAP, bool BIAS, bool SPLIT>
+// Bits lo .. hi - 1 of a word (none if hi <= lo). A tile's mask goes by such
+// words: with two comparisons a score 5 packed documents of 1000 tokens took
+// 17.9 us instead of 15.2, prefixes of 8190 tokens with a bias 430 instead of 381.
+__device__ __forceinline__ uint32_t bit_range(int lo, int hi) {
+  const int f = min(max(lo, 0), 32), t = min(max(hi, 0), 32);
+  return f < t ? (0xffffffffu >> (32 - (t - f))) << f : 0u;
+}
+
+template <int D, int CAP, bool BIAS, bool SPLIT>
 __global__ void __launch_bounds__(384, 1)
     scored_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                        const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ ScoredArgs a) {
@@ -307,8 +318,7 @@ __global__ void __launch_bounds__(384, 1)
     }
     for (int s = 0; s < NST; ++s) {
       ptx::mbar_init(bar(C::B_FULL + s), 1);
-      // two arrivals per tile: one of each slot, or (split) both of the tile's own; and warp 11
-      ptx::mbar_init(bar(C::B_EMPTY + s), a.ranges ? 3 : 2);
+      ptx::mbar_init(bar(C::B_EMPTY + s), a.ranges ? 3 : 2);  // two commits per tile, and warp 11
       ptx::mbar_init(bar(S::B_VOK + s), 1);
     }
     ptx::mbar_init(bar(S::B_JOIN), 4);
@@ -380,6 +390,7 @@ __global__ void __launch_bounds__(384, 1)
         return true;
       };
       int w = blockIdx.x;
+      bool skipped = false;  // the last pair had no second query tile
       while (ok) {
         if (w >= n_pairs) {
           publish(n_pairs, 0, 0, 0);
@@ -409,6 +420,14 @@ __global__ void __launch_bounds__(384, 1)
         // with a bias, the tile of the middle of the pair's rows
         const int near =
             BIAS ? min(max((a.q_start + pr.q0 * 128 + (pr.has1 ? 128 : 64)) / BK - j0, 0), max(nj - 1, 0)) : 0;
+        // Slot 1 waits for no tile of a pair without a query tile of its own. Before
+        // it takes part again all loads so far have landed, so that it can tell
+        // the phase of its next waits.
+        if (!split && pr.has1 && skipped) {
+          for (int u = seq > NST ? seq - NST : 0; ok && u < seq; ++u) ok = wait(C::B_FULL + u % NST, u / NST);
+          if (!ok) break;
+        }
+        skipped = !pr.has1;
         ok = publish(w, j0, nj, near);
         if (!ok) break;
         // the CTA's next turn: the static stride, or a claim on the counter
@@ -472,24 +491,12 @@ __global__ void __launch_bounds__(384, 1)
         if (lane == 0) ptx::mbar_arrive(bar(C::B_WEMPTY + (np & 1)));
         if (w >= n_pairs) break;
         const ScoredPair pr = scored_pair(a, w, nph);
+        const bool sole = !pr.has1;       // a tile has one slot, which gives both commits
         const int first = split ? s : 0;  // my first tile
         for (int j = 0; j < nj; ++j) {
           const int sk = seq, sv = seq + 1;
           seq += 2;
-          if (split && (j & 1) != s) continue;
-          if (s == 1 && !split && !pr.has1) {
-            // no query tile of mine: I keep the ring's pace, so that my next
-            // wait on a stage can tell its phase
-            if (!wait(C::B_FULL + sk % NST, sk / NST) || !wait(C::B_FULL + sv % NST, sv / NST)) {
-              ok = false;
-              break;
-            }
-            if (lane == 0) {
-              ptx::mbar_arrive(bar(C::B_EMPTY + sk % NST));
-              ptx::mbar_arrive(bar(C::B_EMPTY + sv % NST));
-            }
-            continue;
-          }
+          if (split ? (j & 1) != s : (s == 1 && !pr.has1)) continue;
           if ((j == first && !wait(C::B_QFULL + s, qn++)) || !wait(C::B_FULL + sk % NST, sk / NST)) {
             ok = false;
             break;
@@ -506,7 +513,7 @@ __global__ void __launch_bounds__(384, 1)
           }
           commit(C::B_SFULL + s);
           commit(C::B_EMPTY + sk % NST);
-          if (split) commit(C::B_EMPTY + sk % NST);
+          if (sole) commit(C::B_EMPTY + sk % NST);
           if (j + (split ? 2 : 1) >= nj) commit(C::B_QEMPTY + s);
           // with ranges, the V tile once warp 11 has passed it
           if (!wait(C::B_FULL + sv % NST, sv / NST) || (a.ranges && !wait(S::B_VOK + sv % NST, sv / NST))) {
@@ -531,7 +538,7 @@ __global__ void __launch_bounds__(384, 1)
           if (!ok) break;
           commit(C::B_PVDONE + s);
           commit(C::B_EMPTY + sv % NST);
-          if (split) commit(C::B_EMPTY + sv % NST);
+          if (sole) commit(C::B_EMPTY + sv % NST);
           ++tcnt;
         }
         if (!ok) break;
@@ -586,8 +593,7 @@ __global__ void __launch_bounds__(384, 1)
             for (int u = 0; u < 8; ++u) {
 #pragma unroll
               for (int q = 0; q < 4; ++q) {
-                const int f = min(max(rg[u].x - c0 - 32 * q, 0), 32), t = min(max(rg[u].y - c0 - 32 * q, 0), 32);
-                if (f < t) seen[q] |= (0xffffffffu >> (32 - (t - f))) << f;
+                seen[q] |= bit_range(rg[u].x - c0 - 32 * q, rg[u].y - c0 - 32 * q);
               }
             }
             bool cleared = false;
@@ -627,7 +633,7 @@ __global__ void __launch_bounds__(384, 1)
     const uint64_t scale2 = ptx::f32x2(a.scale_log2, a.scale_log2);
     const uint64_t one2 = ptx::f32x2(1.f, 1.f);
     uint64_t cap[4], cap_n[3];
-    if constexpr (CAP) {
+    if constexpr (CAP != 0) {
 #pragma unroll
       for (int u = 0; u < 4; ++u) cap[u] = ptx::f32x2(a.cap_c[u], a.cap_c[u]);
 #pragma unroll
@@ -687,14 +693,18 @@ __global__ void __launch_bounds__(384, 1)
         // polynomial; otherwise s is brought to log2 units here
         bool raw_args = true, narrow = false;
         float mx;
-        if constexpr (CAP) {
-          if (masked) {  // keys out of the row's range have no say in the path taken
-#pragma unroll
-            for (int c = 0; c < BK; ++c)
-              if (c0 + c < rg.x || c0 + c >= rg.y) s[c] = 0.f;
-          }
+        if constexpr (CAP != 0) {
           const float top = row_max(s), low = row_min(s);
-          const float far = fmaxf(top, -low);
+          float far = fmaxf(top, -low);
+          if (masked) {  // keys out of the row's range have no say in the path taken
+            far = 0.f;
+#pragma unroll
+            for (int q = 0; q < BK / 32; ++q) {
+              const uint32_t seen = bit_range(rg.x - c0 - 32 * q, rg.y - c0 - 32 * q);
+#pragma unroll
+              for (int e = 0; e < 32; ++e) far = fmaxf(far, (seen >> e) & 1u ? fabsf(s[32 * q + e]) : 0.f);
+            }
+          }
           const bool wide = __any_sync(0xffffffffu, far > a.cap_fast);
           narrow = !__any_sync(0xffffffffu, far > 0.5f * a.cap_fast);
           raw_args = !wide && !masked && !BIAS;
@@ -704,15 +714,9 @@ __global__ void __launch_bounds__(384, 1)
             ptx::f32x2_split(mul_f32x2(v, cap_poly(v, cap)), y0, y1);
             mx = y0;  // the polynomials rise with s and agree to their error
           } else if (wide) {
-            // small scores beside the large ones keep the polynomial, unless the
-            // cap is so low that the wide form's 2^-22 of it is as good
-            if (a.cap_log2 > kCapFine) {
 #pragma unroll
-              for (int c = 0; c < BK; ++c) s[c] = a.cap_log2 * tanh_any(s[c] * a.cap_in);
-            } else {
-#pragma unroll
-              for (int c = 0; c < BK; ++c) s[c] = a.cap_log2 * tanh_wide(s[c] * a.cap_in);
-            }
+            for (int c = 0; c < BK; ++c)
+              s[c] = a.cap_log2 * (CAP == kCapHigh ? tanh_any(s[c] * a.cap_in) : tanh_wide(s[c] * a.cap_in));
             if constexpr (BIAS) scale_and_bias(s, [&](uint64_t) { return one2; }, slope2, at, c0);
           } else if constexpr (BIAS) {
             if (narrow) scale_and_bias(s, [&](uint64_t v) { return cap_poly_narrow(v, cap_n); }, slope2, at, c0);
@@ -730,10 +734,14 @@ __global__ void __launch_bounds__(384, 1)
         }
         if (masked) {
 #pragma unroll
-          for (int c = 0; c < BK; ++c)
-            if (c0 + c < rg.x || c0 + c >= rg.y) s[c] = ninf;
+          for (int q = 0; q < BK / 32; ++q) {
+            const uint32_t seen = bit_range(rg.x - c0 - 32 * q, rg.y - c0 - 32 * q);
+#pragma unroll
+            for (int e = 0; e < 32; ++e)
+              if (!((seen >> e) & 1u)) s[32 * q + e] = ninf;
+          }
         }
-        if constexpr (CAP) {
+        if constexpr (CAP != 0) {
           if (!raw_args) mx = row_max(s);
         } else {
           mx = row_max(s);
@@ -786,7 +794,7 @@ __global__ void __launch_bounds__(384, 1)
           }
         };
         using Plain = std::integral_constant<int, 0>;
-        if constexpr (CAP && !BIAS) {
+        if constexpr (CAP != 0 && !BIAS) {
           if (raw_args && narrow) exp_pass(std::integral_constant<int, 1>{}, one2);
           else if (raw_args) exp_pass(std::integral_constant<int, 2>{}, one2);
           else exp_pass(Plain{}, one2);

@@ -108,7 +108,7 @@ struct ScoredMaps {
   CUtensorMap q, k, v;
 };
 
-template <int D, bool CAP, bool BIAS, bool SPLIT>
+template <int D, int CAP, bool BIAS, bool SPLIT>
 int launch_scored_t(const ScoredMaps& t, const ScoredArgs& a, int dev, int grid, cudaStream_t st) {
   using C = AttnCfg<D, 128>;
   auto kern = scored_attn_kernel<D, CAP, BIAS, SPLIT>;
@@ -120,18 +120,20 @@ int launch_scored_t(const ScoredMaps& t, const ScoredArgs& a, int dev, int grid,
   return SPARSED_OK;
 }
 
-template <int D, bool CAP, bool BIAS>
+template <int D, int CAP, bool BIAS>
 int launch_scored_s(const ScoredMaps& t, const ScoredArgs& a, int dev, int grid, cudaStream_t st) {
   return a.qpp == 1 ? launch_scored_t<D, CAP, BIAS, true>(t, a, dev, grid, st)
                     : launch_scored_t<D, CAP, BIAS, false>(t, a, dev, grid, st);
 }
+template <int D, int CAP>
+int launch_scored_b(const ScoredMaps& t, const ScoredArgs& a, int dev, int grid, cudaStream_t st) {
+  return a.slopes ? launch_scored_s<D, CAP, true>(t, a, dev, grid, st) : launch_scored_s<D, CAP, false>(t, a, dev, grid, st);
+}
 template <int D>
-int launch_scored(const ScoredMaps& t, const ScoredArgs& a, bool cap, int dev, int grid, cudaStream_t st) {
-  if (cap)
-    return a.slopes ? launch_scored_s<D, true, true>(t, a, dev, grid, st)
-                    : launch_scored_s<D, true, false>(t, a, dev, grid, st);
-  return a.slopes ? launch_scored_s<D, false, true>(t, a, dev, grid, st)
-                  : launch_scored_s<D, false, false>(t, a, dev, grid, st);
+int launch_scored(const ScoredMaps& t, const ScoredArgs& a, float softcap, int dev, int grid, cudaStream_t st) {
+  if (softcap > kCapLowMost) return launch_scored_b<D, kCapHigh>(t, a, dev, grid, st);
+  if (softcap > 0.f) return launch_scored_b<D, kCapLow>(t, a, dev, grid, st);
+  return launch_scored_b<D, kCapNone>(t, a, dev, grid, st);
 }
 
 // Capped scores in log2 units: y = s * P(s^2) while |s| * scale / cap <= 0.5,
@@ -505,7 +507,7 @@ int sparsed_scored_attn(const uint16_t* Q, size_t q_stride_h, size_t q_stride_l,
     SP_CUDA(cudaMemsetAsync(a.sched, 0, sizeof(int), st));
   }
   const int grid = static_cast<int>(turns < sms ? turns : sms);
-  return d == 64 ? launch_scored<64>(t, a, softcap > 0.f, dev, grid, st) : launch_scored<128>(t, a, softcap > 0.f, dev, grid, st);
+  return d == 64 ? launch_scored<64>(t, a, softcap, dev, grid, st) : launch_scored<128>(t, a, softcap, dev, grid, st);
 }
 
 }  // extern "C"

@@ -138,13 +138,19 @@ class RingWaiter:
         self.top = max(self.top, seq)
 
 
-def ring_waits(stages, split, turns, slot, follows=True):
+def ring_waits(stages, split, turns, slot, lands=True):
     """The loads that an issuer of scored_attn_kernel waits for: K_j is load
-    2 j, V_j load 2 j + 1. turns: (tiles, whether slot 1 has a query tile)."""
-    w, seq = RingWaiter(stages), 0
+    2 j, V_j load 2 j + 1. turns: (tiles, whether slot 1 has a query tile).
+    lands: the producer waits for its loads before a turn that slot 1 takes
+    part in again, and the issuer learns of the turn after that."""
+    w, seq, skipped = RingWaiter(stages), 0, False
     for tiles, has1 in turns:
+        if lands and not split and has1 and skipped:
+            w.waited.update(range(seq))
+            w.top = max(w.top, seq - 1)
+        skipped = not has1
         for j in range(tiles):
-            if (j & 1) == slot if split else (slot == 0 or has1 or follows):
+            if (j & 1) == slot if split else (slot == 0 or has1):
                 w.wait(seq)
                 w.wait(seq + 1)
             seq += 2
@@ -174,9 +180,10 @@ def test_the_ring_model_finds_the_unsafe_forms():
     with pytest.raises(AssertionError, match="may pass"):
         ring_waits(5, True, [(8, False)], 0)
     with pytest.raises(AssertionError, match="may pass"):
-        ring_waits(5, False, [(3, False), (3, True)], 1, follows=False)
-    # the issuers do follow, and the split form has its own ring
+        ring_waits(5, False, [(3, False), (3, True)], 1, lands=False)
+    # the split form has its own ring, and the producer waits ahead of the turn's publication
     body = kernel_body(source("scored_kernel.cuh"), "scored_attn_kernel")
     assert "constexpr int NST = SPLIT ? S::NST_SPLIT : S::NST;" in body
-    skip = body[body.index("if (s == 1 && !split && !pr.has1) {"):]
-    assert skip.index("C::B_FULL + sk % NST") < skip.index("C::B_FULL + sv % NST") < skip.index("continue;")
+    wait = body.index("if (!split && pr.has1 && skipped) {")
+    assert body.index("wait(C::B_FULL + u % NST, u / NST)", wait) < body.index("skipped = !pr.has1;", wait) \
+        < body.index("ok = publish(w, j0, nj, near);", wait)
