@@ -237,6 +237,21 @@ __device__ __forceinline__ void reg_fence16(uint32_t (&r)[16]) {
 __device__ __forceinline__ int cache_len(const CacheArgs& a, int n) { return min(max(a.lengths[n], 0), a.C); }
 __device__ __forceinline__ int cache_tiles(const CacheArgs& a, int len) { return (len + a.tile - 1) / a.tile; }
 
+// Position of query token b of sequence n, and the nearest cached one to it. A
+// row's distances are taken from the latter (scored_attn does the same): they
+// are all shorter by the same amount, which its log-sum loses at the end.
+__device__ __forceinline__ int query_position(const CacheArgs& a, int n, int len, int b) {
+  return (a.q_start ? min(max(a.q_start[n], -(1 << 29)), 1 << 29) : len - a.B) + b;
+}
+__device__ __forceinline__ int nearest_key(int at, int len) { return min(max(at, 0), len - 1); }
+// What row rr of a kv head's rows loses (natural units).
+__device__ __forceinline__ float beyond_keys(const CacheArgs& a, int n, int hk, int len, int rr) {
+  if (!a.slopes) return 0.f;
+  const int hg = rr / a.B;
+  const int at = query_position(a, n, len, rr - hg * a.B), in = nearest_key(at, len);
+  return at == in ? 0.f : a.slopes[hk * a.group + hg] * static_cast<float>(abs(at - in));
+}
+
 // An item's length in the runs' unit: its tiles and the toll.
 __device__ __forceinline__ int item_units(const CacheArgs& a, int nt) { return nt > 0 ? nt + a.toll : 0; }
 
@@ -867,7 +882,9 @@ __global__ void __launch_bounds__(CacheCfg<D, Q>::THREADS, 1)
         const float f = (empty ? 0.f : share / L) * pow2i(vref);
         if (row_valid && half == 0 && (!FEW || cc == 0)) {
           const float lse2 = empty ? ninf : M - kPShift + ptx::lg2(L);
-          if (whole) a.lse[grow0 + r] = lse2 * 0.69314718055994530942f;
+          if (whole)
+            a.lse[grow0 + r] = lse2 * 0.69314718055994530942f -
+                               (MODE != 0 ? beyond_keys(a, part.n, part.hk, part.len, part.rt * 128 + r) : 0.f);
           else a.l_part[prow0 + r] = lse2;
         }
 #pragma unroll 1
@@ -951,7 +968,7 @@ __global__ void __launch_bounds__(CacheCfg<D, Q>::THREADS, 1)
         const int rr = min(part.rt * 128 + r, a.R - 1);
         const int hg = rr / a.B;
         if (a.slopes) slope2 = a.slopes[part.hk * a.group + hg] * 1.44269504088896340736f;
-        at = (a.q_start ? min(max(a.q_start[part.n], -(1 << 29)), 1 << 29) : part.len - a.B) + (rr - hg * a.B);
+        at = nearest_key(query_position(a, part.n, part.len, rr - hg * a.B), part.len);
       }
       m = ninf;
       l = 0.f;
@@ -1120,8 +1137,10 @@ __global__ void __launch_bounds__(CacheCfg<D, Q>::THREADS, 1)
 // results. Every CTA waits before it ends, also one that has nothing to join:
 // what follows on the stream is ordered behind this grid alone, which must not
 // end before the attention kernel's last rows are written.
+// BIAS: with slopes, a row loses what beyond_keys says (as code that a call
+// without them does not run it takes 0.6 us of a single token's 17).
 constexpr int kMergeRows = 10;
-template <int D>
+template <int D, bool BIAS>
 __global__ void __launch_bounds__(kCacheMaxCtas) cache_merge_kernel(const __grid_constant__ CacheArgs a, int runs) {
   constexpr int V = D / 32;  // elements of a lane
   constexpr int WARPS = kCacheMaxCtas / 32;
@@ -1139,7 +1158,7 @@ __global__ void __launch_bounds__(kCacheMaxCtas) cache_merge_kernel(const __grid
     return;
   }
   const long grow0 = (static_cast<long>(n) * a.Hkv + hk) * a.R + rt * 128;
-  const int nt = cache_tiles(a, cache_len(a, n));
+  const int len = cache_len(a, n), nt = cache_tiles(a, len);
   if (nt == 0) {
     ptx::grid_dep_wait();  // O and LSE may still be read by what ran before the attention kernel
     for (int r = r0 + warp; r < r1; r += WARPS) {
@@ -1214,7 +1233,10 @@ __global__ void __launch_bounds__(kCacheMaxCtas) cache_merge_kernel(const __grid
     uint32_t* dst = reinterpret_cast<uint32_t*>(a.o + (grow0 + r) * D) + lane * (V / 2);
 #pragma unroll
     for (int e = 0; e < V / 2; ++e) dst[e] = ptx::pack_bf16x2(acc[2 * e] * inv, acc[2 * e + 1] * inv);
-    if (lane == 0) a.lse[grow0 + r] = sum == 0.f ? ninf : (base + ptx::lg2(sum)) * 0.69314718055994530942f;
+    if (lane == 0)
+      a.lse[grow0 + r] = sum == 0.f ? ninf
+                                    : (base + ptx::lg2(sum)) * 0.69314718055994530942f -
+                                          (BIAS ? beyond_keys(a, n, hk, len, rt * 128 + r) : 0.f);
   }
 }
 

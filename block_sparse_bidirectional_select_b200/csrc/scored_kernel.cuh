@@ -662,9 +662,18 @@ __global__ void __launch_bounds__(384, 1)
       // my row's keys, and those that all 32 rows of the warp see
       const int2 rg = scored_range(a, grow, true);
       const int all_lo = __reduce_max_sync(0xffffffffu, rg.x), all_hi = __reduce_min_sync(0xffffffffu, rg.y);
-      float slope2 = 0.f;
-      if constexpr (BIAS) slope2 = a.slopes[h] * 1.44269504088896340736f;
-      const int at = a.q_start + grow;
+      // A row that stands outside its keys is moved to the nearest of them: all
+      // its distances shrink by the same amount, which is taken off its log-sum.
+      // Else the differences between the keys would drown in the rounding of
+      // large biases.
+      float slope2 = 0.f, beyond = 0.f;
+      int at = a.q_start + grow;
+      if constexpr (BIAS) {
+        slope2 = a.slopes[h] * 1.44269504088896340736f;
+        const int in = rg.x < rg.y ? min(max(at, rg.x), rg.y - 1) : at;
+        if (in != at) beyond = a.slopes[h] * static_cast<float>(abs(at - in));
+        at = in;
+      }
       float m = ninf;  // running row max, log2 units
       float l = 0.f;   // running row sum
       const int first = split ? slot : 0, step = split ? 2 : 1;  // my tiles
@@ -881,7 +890,7 @@ __global__ void __launch_bounds__(384, 1)
             o_dst[c * 4 + u] = make_uint4(pk[4 * u], pk[4 * u + 1], pk[4 * u + 2], pk[4 * u + 3]);
         }
       }
-      if (row_valid) *lse_dst = empty ? ninf : (m + ptx::lg2(l)) * 0.69314718055994530942f;
+      if (row_valid) *lse_dst = empty ? ninf : (m + ptx::lg2(l)) * 0.69314718055994530942f - beyond;
       // the next item's first PV overwrites O_s only after this warp's next
       // PFULL arrival, which follows the loads above (tcgen05.wait::ld)
     }

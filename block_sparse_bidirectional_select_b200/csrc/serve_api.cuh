@@ -187,6 +187,22 @@ int make_map_cache(CUtensorMap* m, const uint8_t* ptr, long H, int C, int d, int
   return SPARSED_OK;
 }
 
+// The merge kernel asks for the attention kernel's split of an SM's memory: its
+// CTAs can then sit beside the last runs, and no SM changes its split.
+template <int D, bool BIAS>
+int launch_cache_merge(const CacheArgs& a, int dev, unsigned items, int runs, cudaStream_t st) {
+  static std::atomic<uint64_t> done{0};
+  const uint64_t bit = dev < kMaxDevices ? 1ull << dev : 0;
+  if (!(done.load(std::memory_order_acquire) & bit)) {
+    SP_CUDA(cudaFuncSetAttribute(cache_merge_kernel<D, BIAS>, cudaFuncAttributePreferredSharedMemoryCarveout,
+                                 cudaSharedmemCarveoutMaxShared));
+    done.fetch_or(bit, std::memory_order_release);
+  }
+  const unsigned row_groups = static_cast<unsigned>(cdiv(a.R < 128 ? a.R : 128, kMergeRows));
+  return launch_k(cache_merge_kernel<D, BIAS>, dim3(items, static_cast<unsigned>(a.N), row_groups),
+                  dim3(kCacheMaxCtas), 0, st, runs > 0, a, runs > 0 ? runs : 1);
+}
+
 template <int D, int MODE, int Q>
 int launch_cache_attn(const uint8_t* k8, const uint8_t* v8, CacheArgs& a, int dev, int sms, cudaStream_t st) {
   using C = CacheCfg<D, Q>;
@@ -210,18 +226,8 @@ int launch_cache_attn(const uint8_t* k8, const uint8_t* v8, CacheArgs& a, int de
     kern<<<runs, C::THREADS, C::SMEM_BYTES, st>>>(tk, tv, a);
     SP_CUDA(cudaGetLastError());
   }
-  // The merge kernel asks for the attention kernel's split of an SM's memory:
-  // its CTAs can then sit beside the last runs, and no SM changes its split.
-  static std::atomic<uint64_t> merge_done{0};
-  const uint64_t bit = dev < kMaxDevices ? 1ull << dev : 0;
-  if (!(merge_done.load(std::memory_order_acquire) & bit)) {
-    SP_CUDA(cudaFuncSetAttribute(cache_merge_kernel<D>, cudaFuncAttributePreferredSharedMemoryCarveout,
-                                 cudaSharedmemCarveoutMaxShared));
-    merge_done.fetch_or(bit, std::memory_order_release);
-  }
-  const unsigned row_groups = static_cast<unsigned>(cdiv(a.R < 128 ? a.R : 128, kMergeRows));
-  return launch_k(cache_merge_kernel<D>, dim3(items, static_cast<unsigned>(a.N), row_groups), dim3(kCacheMaxCtas), 0,
-                  st, runs > 0, a, runs > 0 ? runs : 1);
+  return a.slopes ? launch_cache_merge<D, true>(a, dev, items, runs, st)
+                  : launch_cache_merge<D, false>(a, dev, items, runs, st);
 }
 
 }  // namespace

@@ -68,3 +68,22 @@ def test_small_scores_beside_scores_near_the_cap(d, softcap):
         assert ((lse.double() - want).abs() <= tol).all(), float(((lse.double() - want).abs() / tol).max())
         _, lse = sp.cache_attn(q[None], cache, i32([1]), scale=1.0, softcap=softcap, slopes=zero)
         assert ((lse.double() - want).abs() <= tol).all(), float(((lse.double() - want).abs() / tol).max())
+
+
+@pytest.mark.parametrize("q_start", [10 ** 6, -10 ** 6, 2 ** 24 + 77, 2 ** 29, -2 ** 29])
+@pytest.mark.parametrize("softcap", [0.0, 30.0])
+def test_positions_far_from_the_keys(q_start, softcap):
+    """The distances to all keys are large and their differences small: what a chunk of keys far from the queries is."""
+    g = gen(73)
+    slopes = torch.tensor([1.0, 2.0 ** -4, 2.0 ** -9, 0.0], device="cuda")
+    for Lq, H in ((100, 4), (700, 4)):
+        q, k, v = randn(g, H, Lq, 64), randn(g, 2, 900, 64), randn(g, 2, 900, 64)
+        check_scored(q, k, v, softcap, slopes, q_start=q_start)
+        lo = torch.randint(-20, 900, (Lq,), generator=g)
+        ranges = torch.stack([lo, lo + torch.randint(-2, 400, (Lq,), generator=g)], 1).to(torch.int32).cuda()
+        check_scored(q, k, v, softcap, slopes, ranges, q_start=q_start)
+    c = random_cache(g, 3, 2, 1088, 128)
+    for B in (1, 20, 70):
+        check_cache_attn(randn(g, 3, 4, B, 128), c, [1088, 1, 700], softcap, slopes, [q_start, q_start, 0])
+    long = random_cache(g, 1, 2, 32768, 128)      # its parts are joined
+    check_cache_attn(randn(g, 1, 4, 3, 128), long, [32700], softcap, slopes, [q_start])
