@@ -185,19 +185,27 @@ __device__ __forceinline__ void scale_and_bias(float (&s)[N], Mul mul, float slo
   }
 }
 
-template <int N>
+// Three-input maximum that is NaN if an input is (one instruction).
+__device__ __forceinline__ float max3_nan(float a, float b, float c) {
+  float d;
+  asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+// The largest of a row's scores; NAN_TOO: NaN if one is, else NaNs are left out.
+template <bool NAN_TOO = false, int N>
 __device__ __forceinline__ float row_max(const float (&s)[N]) {
+  auto max3 = [](float a, float b, float c) { return NAN_TOO ? max3_nan(a, b, c) : ptx::max3(a, b, c); };
   float mx0 = s[0], mx1 = s[1], mx2 = s[2], mx3 = s[3];
 #pragma unroll
   for (int c = 4; c < N; c += 8) {
-    mx0 = ptx::max3(mx0, s[c], s[c + 1]);
-    mx1 = ptx::max3(mx1, s[c + 2], s[c + 3]);
+    mx0 = max3(mx0, s[c], s[c + 1]);
+    mx1 = max3(mx1, s[c + 2], s[c + 3]);
     if (c + 4 < N) {
-      mx2 = ptx::max3(mx2, s[c + 4], s[c + 5]);
-      mx3 = ptx::max3(mx3, s[c + 6], s[c + 7]);
+      mx2 = max3(mx2, s[c + 4], s[c + 5]);
+      mx3 = max3(mx3, s[c + 6], s[c + 7]);
     }
   }
-  return fmaxf(fmaxf(mx0, mx1), fmaxf(mx2, mx3));
+  return NAN_TOO ? max3_nan(max3_nan(mx0, mx1, mx2), mx3, mx3) : fmaxf(fmaxf(mx0, mx1), fmaxf(mx2, mx3));
 }
 // Three-input minimum (one instruction).
 __device__ __forceinline__ float min3(float a, float b, float c) {
@@ -750,12 +758,16 @@ __global__ void __launch_bounds__(384, 1)
               if (!((seen >> e) & 1u)) s[32 * q + e] = ninf;
           }
         }
+        // with a bias a NaN shows in mx, so that its tile does not pass for one of
+        // zeros below; the running maximum leaves it out either way. Rows past the
+        // last, which see padding too, have no say in the warp's votes.
         if constexpr (CAP != 0) {
-          if (!raw_args) mx = row_max(s);
+          if (!raw_args) mx = row_max<BIAS>(s);
         } else {
-          mx = row_max(s);
+          mx = row_max<BIAS>(s);
           if constexpr (!BIAS) mx *= a.scale_log2;  // scale_log2 > 0
         }
+        if (BIAS && !row_valid) mx = ninf;
         const float m_new = fmaxf(m, mx);
         if (jj == first) {
           m = m_new;

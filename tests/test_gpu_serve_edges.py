@@ -87,3 +87,23 @@ def test_positions_far_from_the_keys(q_start, softcap):
         check_cache_attn(randn(g, 3, 4, B, 128), c, [1088, 1, 700], softcap, slopes, [q_start, q_start, 0])
     long = random_cache(g, 1, 2, 32768, 128)      # its parts are joined
     check_cache_attn(randn(g, 1, 4, 3, 128), long, [32700], softcap, slopes, [q_start])
+
+
+@pytest.mark.parametrize("H", [2, 40])
+@pytest.mark.parametrize("softcap", [0.0, 30.0])
+def test_a_visible_nan_reaches_its_rows_however_far(H, softcap):
+    g = gen(74)
+    L = 1000
+    q, k, v = randn(g, H, L, 64), randn(g, 2, L, 64), randn(g, 2, L, 64)
+    k[:, 20, 5] = math.nan
+    steep = torch.full((H,), 10.0, device="cuda")
+    ranges = torch.tensor([[0, L]] * 600 + [[21, L]] * 400, dtype=torch.int32, device="cuda")
+    o, lse = sp.scored_attn(q, k, v, softcap=softcap, slopes=steep, ranges=ranges)
+    assert torch.isnan(o[:, :600]).all() and torch.isnan(lse[:, :600]).all()
+    assert not torch.isnan(o[:, 600:]).any() and not torch.isnan(lse[:, 600:]).any()
+    c = random_cache(g, 1, 2, 1024, 64)
+    c.k8.view(torch.uint8)[0, :, 20, 5] = 0x7F
+    for B in (1, 40):
+        o, lse = sp.cache_attn(randn(g, 1, 2, B, 64), c, i32([1000]), softcap=softcap, slopes=steep[:2])
+        assert torch.isnan(o).all() and torch.isnan(lse).all()
+    sp.device_check()
