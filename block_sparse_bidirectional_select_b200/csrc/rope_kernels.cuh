@@ -9,12 +9,13 @@
 // elements from 2J on are copied.
 //
 // The angle. inv_j / 2 pi is given as a 64-bit binary fraction of a turn, so
-// position * fraction in 64-bit integers drops whole turns exactly and the
-// upper 32 bits are the signed fraction of a turn. An fp32 product would be
-// off by position * 2^-24 (0.06 rad at a position of 10^6); this one is off by
-// 2^-32 turns plus position * 2^-53 at most, and fp32 by 2^-23 rad. Reduced to
-// [-pi, pi), the hardware sine and cosine are off by 2^-21, an eight-thousandth
-// of the result's rounding to bf16.
+// position * fraction in 64-bit integers drops whole turns exactly. An fp32
+// product would be off by position * 2^-24 (0.06 rad at a position of 10^6);
+// this one is off by position * 2^-53 turns at most. The nearest quarter turn
+// is taken off in integers too, before the rest becomes an fp32: so the sine
+// and the cosine are right to a few fp32 roundings of themselves, also where
+// they are nearly 0 (the hardware sine of the whole angle is off by 2^-21 of 1,
+// more than a bf16 step of a result below 2^-12, for 2% less time).
 #pragma once
 
 #include "ptx_sm100.cuh"
@@ -56,13 +57,29 @@ __device__ __forceinline__ uint16_t f32_to_bf16(float f) {
   return static_cast<uint16_t>(ptx::pack_bf16x2(f, 0.f) & 0xFFFFu);
 }
 
+// Sine and cosine of turns / 2^64 turns: of the angle t left by the nearest
+// quarter turn, |t| <= pi / 4, by their Taylor series up to t^9 and t^8, which
+// end 2.5e-9 (of the sine) and 2.5e-8 from them.
+__device__ __forceinline__ void turn_sincos(uint64_t turns, float& sn, float& cs) {
+  const uint32_t quarter = static_cast<uint32_t>((turns + (1ull << 61)) >> 62);  // mod 4
+  const int64_t rest = static_cast<int64_t>(turns - (static_cast<uint64_t>(quarter) << 62));
+  const float t = static_cast<float>(rest) * (0x1p-64f * 6.283185307179586f), w = t * t;
+  const float s = fmaf(fmaf(fmaf(fmaf(1.f / 362880, w, -1.f / 5040), w, 1.f / 120), w, -1.f / 6) * w, t, t);
+  const float c = fmaf(fmaf(fmaf(fmaf(1.f / 40320, w, -1.f / 720), w, 1.f / 24), w, -0.5f), w, 1.f);
+  sn = quarter & 1 ? c : s;
+  cs = quarter & 1 ? s : c;
+  if (quarter & 2) sn = -sn;
+  if ((quarter + 1) & 2) cs = -cs;
+}
+
 // A thread owns one unit of eight pairs of one token: it takes their sines and
 // cosines once and turns that unit of every head of its CTA's share. VEC: all
 // addresses are 16-byte aligned and, with split halves, J is a multiple of 8,
 // so a unit is two 16-byte loads and stores; otherwise element by element.
 // Bound by memory: 2 bytes read and written per element. 32768 tokens of 32
-// heads (537 MB) take 94 us, 5.7 TB/s, 89% of a copy; a CTA of few heads pays
-// its sines again (16, 8, 4, 2 heads: 96, 97, 101, 137 us, measured with sincospi).
+// heads (537 MB) take 97 us, 5.5 TB/s, 86% of a copy (95 us with the hardware's
+// sine and cosine); a CTA of few heads pays its sines again (16, 8, 4, 2 heads:
+// 97, 99, 104, 141 us).
 template <bool INTERLEAVED, bool VEC>
 __global__ void __launch_bounds__(kRopeThreads) rope_axes_kernel(const __grid_constant__ RopeArgs a) {
   const int tokens = kRopeThreads / a.units;
@@ -88,10 +105,7 @@ __global__ void __launch_bounds__(kRopeThreads) rope_axes_kernel(const __grid_co
     const int j = min(j0 + e, a.J - 1);
     const long p = a.pos[static_cast<long>(a.axis[j]) * a.L + l] * static_cast<long>(a.sign);
     const uint64_t turns = static_cast<uint64_t>(p) * a.turn[j];
-    // signed fraction of a turn -> radians in [-pi, pi)
-    const float t = static_cast<float>(static_cast<int32_t>(turns >> 32)) * (0x1p-32f * 6.283185307179586f);
-    sn[e] = __sinf(t);
-    cs[e] = __cosf(t);
+    turn_sincos(turns, sn[e], cs[e]);
   }
   if constexpr (VEC) {
     // the unit's two 16-byte parts

@@ -574,7 +574,8 @@ int sparsed_losa_block(const uint16_t* Qs, const uint16_t* Ks, const uint16_t* V
  * the i-th pair of its axis, or j / J when shared_ladder != 0:
  *   a' = a cos - b sin,  b' = b cos + a sin    (fp32, rounded once)
  * inverse != 0 turns the other way, which is also the gradient's rotation.
- * Angles are exact to 2^-32 turns plus |position| * 2^-53, sines to 2^-20.
+ * Angles are exact to |position| * 2^-53 turns, sines and cosines to 2^-21 of
+ * themselves.
  * d is a multiple of 8 in 8..512, n_axes <= 8, J <= 128, theta >= 1. Any
  * alignment and strides; fastest with J and all strides multiples of 8 and 16-byte aligned X, Y. */
 int sparsed_rope_axes(const uint16_t* X, size_t x_stride_h, size_t x_stride_l,

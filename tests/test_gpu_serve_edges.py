@@ -107,3 +107,25 @@ def test_a_visible_nan_reaches_its_rows_however_far(H, softcap):
         o, lse = sp.cache_attn(randn(g, 1, 2, B, 64), c, i32([1000]), softcap=softcap, slopes=steep[:2])
         assert torch.isnan(o).all() and torch.isnan(lse).all()
     sp.device_check()
+
+
+@pytest.mark.parametrize("shared,inter", [(False, False), (True, True)])
+def test_rope_of_single_elements_next_to_a_quadrant(shared, inter):
+    """Pairs with one element 0: the result is x cos t or x sin t, right to its
+    own last bit also where that is nearly 0. The angle is off by position *
+    2^-53 turns and the reference's by position * 2^-52 rad (together below
+    position * 2^-50 rad), the sine by a few fp32 roundings of itself, the
+    product by one, the result by half a bf16 step."""
+    g = gen(75)
+    L, d = 40000, 64
+    x = (torch.rand(2, L, d, generator=g) + 0.5).to(torch.bfloat16).cuda()
+    first = torch.arange(d, device="cuda") % 2 == 0 if inter else torch.arange(d, device="cuda") < d // 2
+    x[0, :, ~first] = 0
+    x[1, :, first] = 0
+    pos = torch.arange(-L // 2, L - L // 2, dtype=torch.int32, device="cuda")[None].contiguous()
+    for theta in (10000.0, 1e6):
+        y = sp.rope_axes(x, pos, (32,), theta=theta, interleaved=inter, shared_ladder=shared)
+        ref, amp = R.rope(x, pos, (32,), float(torch.tensor(theta)), inter, shared, False)
+        tol = (R.U_BF16 + 2.0 ** -20) * ref.abs() + 2.0 ** -50 * pos[0].abs().double()[None, :, None] * amp + 2.0 ** -133
+        err = (y.double() - ref).abs()
+        assert (err <= tol).all(), f"{int((err > tol).sum())} elements, {float((err / tol).max()):.1f} of the bound"
