@@ -129,3 +129,35 @@ def test_rope_of_single_elements_next_to_a_quadrant(shared, inter):
         tol = (R.U_BF16 + 2.0 ** -20) * ref.abs() + 2.0 ** -50 * pos[0].abs().double()[None, :, None] * amp + 2.0 ** -133
         err = (y.double() - ref).abs()
         assert (err <= tol).all(), f"{int((err > tol).sum())} elements, {float((err / tol).max()):.1f} of the bound"
+
+
+@pytest.mark.parametrize("d,N,Hq,Hkv,B,C,bias", [(128, 1, 8, 2, 1, 16384, False), (64, 1, 2, 1, 1, 32768, False),
+                                                 (128, 2, 4, 4, 16, 8192, True), (128, 1, 2, 2, 64, 16384, False),
+                                                 (64, 3, 2, 1, 40, 8192, False), (128, 1, 4, 1, 70, 16384, False)])
+def test_long_caches_whose_blocks_differ(d, N, Hq, Hkv, B, C, bias):
+    """Block j of V fills the columns j mod 64 and no others, so a column holds a few blocks of the cache and a block
+    that is left out, or that is given another's scale, shows there. That it does is checked with such a mistake in
+    the reference."""
+    g = gen(76 + B)
+    c = random_cache(g, N, Hkv, C, d)
+    blocks = C // 64
+    at = torch.arange(blocks)
+    own = (torch.arange(d)[None] % 64 == at[:, None] % 64).float()                  # [blocks, d]
+    v = (torch.rand(N, Hkv, blocks, 64, d, generator=g) * 0.2 + 0.9) * own[:, None]
+    scale = 2.0 ** torch.randint(-8, -5, (N, Hkv, blocks), generator=g).float()
+    c.v_scale.copy_(scale)
+    c.v8.copy_((v / scale[..., None, None]).reshape(N, Hkv, C, d).to(torch.float8_e4m3fn))
+    c.k8.copy_((torch.randn(c.k8.shape, generator=g) * 20).to(torch.float8_e4m3fn))
+    lengths = [C - 1 - 777 * n for n in range(N)]
+    q, slopes = randn(g, N, Hq, B, d), slopes_of(Hq) * 1e-4 if bias else None
+    o, lse = check_cache_attn(q, c, lengths, 0.0, slopes)
+    k0, v0 = (R.dequant(x8, sc)[0, 0, :lengths[0]] for x8, sc in ((c.k8, c.k_scale), (c.v8, c.v_scale)))
+    lo, pos = torch.zeros(B, dtype=torch.long, device="cuda"), torch.arange(B, device="cuda") + lengths[0] - B
+    for j in (0, 1, blocks // 2, blocks - 2):
+        for factor in (0.0, 2.0):
+            wrong = v0.clone()
+            wrong[64 * j:64 * j + 64] *= factor
+            ref = R.attend(q[0, 0], k0, wrong, lo, lo + lengths[0], pos, sp.default_scale(d), 0.0,
+                           None if slopes is None else float(slopes[0]))
+            with pytest.raises(AssertionError, match="O off"):
+                R.assert_attention(o[0, 0], lse[0, 0], ref)
