@@ -54,6 +54,22 @@ uint64_t turn_fraction(double x) {
   return static_cast<uint64_t>(std::ldexp(x, 64) < 18446744073709549568.0 ? std::ldexp(x, 64) : 18446744073709549568.0);
 }
 
+// Whether two of the H x L rows of d elements at h * sh + l * sl share one.
+bool rows_overlap(long H, size_t sh, long L, size_t sl, size_t d) {
+  if (H > L) return rows_overlap(L, sl, H, sh, d);
+  // the usual layouts: the rows of one dimension side by side, those of the other past them
+  if (sl >= d && (H == 1 || sh >= sl * static_cast<size_t>(L - 1) + d)) return false;
+  if (sh >= d && (L == 1 || sl >= sh * static_cast<size_t>(H - 1) + d)) return false;
+  if (L > 1 && sl < d) return true;
+  for (long h = 1; h < H; ++h) {  // the rows l of head 0 next to row 0 of head h
+    const size_t at = static_cast<size_t>(h) * sh;
+    const size_t l = L > 1 ? at / sl : 0;
+    if (l < static_cast<size_t>(L) && at - l * sl < d) return true;
+    if (l + 1 < static_cast<size_t>(L) && (l + 1) * sl - at < d) return true;
+  }
+  return false;
+}
+
 template <bool I, bool V>
 int launch_rope(const RopeArgs& a, dim3 grid, cudaStream_t st) {
   rope_axes_kernel<I, V><<<grid, kRopeThreads, 0, st>>>(a);
@@ -249,6 +265,7 @@ int sparsed_rope_axes(const uint16_t* X, size_t x_stride_h, size_t x_stride_l, c
   if (J > kRopeMaxPairs) return SPARSED_ERR_UNSUPPORTED;
   if (H == 0 || L == 0) return SPARSED_OK;
   if (!X || !Y || !positions || !aligned2(X) || !aligned2(Y) || !aligned4(positions)) return SPARSED_ERR_INVALID_ARG;
+  if (rows_overlap(H, y_stride_h, L, y_stride_l, static_cast<size_t>(d))) return SPARSED_ERR_INVALID_ARG;
   int dev = 0, sms = 0;
   SP_TRY(current_device(&dev, &sms));
   RopeArgs a;

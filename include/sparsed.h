@@ -577,7 +577,7 @@ int sparsed_losa_block(const uint16_t* Qs, const uint16_t* Ks, const uint16_t* V
  * Angles are exact to |position| * 2^-53 turns, sines and cosines to 2^-21 of
  * themselves.
  * d is a multiple of 8 in 8..512, n_axes <= 8, J <= 128, theta >= 1. Any
- * alignment and strides; fastest with J and all strides multiples of 8 and 16-byte aligned X, Y. */
+ * alignment and strides (X's may be 0; the rows of Y must not overlap); fastest with J and all strides multiples of 8 and 16-byte aligned X, Y. */
 int sparsed_rope_axes(const uint16_t* X, size_t x_stride_h, size_t x_stride_l,
                       const int32_t* positions, int n_axes, const int* sections,
                       int H, int L, int d, float theta, int interleaved, int shared_ladder, int inverse,
