@@ -89,7 +89,7 @@ struct CacheArgs {
   int toll;                        // what beginning an item costs, in tiles
   float scale_log2;                // above 0
   const float* slopes;             // or null
-  float cap_c[4], cap_n[3];        // as ScoredArgs
+  float cap_c[4];                  // as ScoredArgs
   float cap_fast, cap_in, cap_log2;
   uint16_t* o;                     // [N, Hkv * group, B, D]
   float* lse;

@@ -154,10 +154,10 @@ int launch_scored(const ScoredMaps& t, const ScoredArgs& a, float softcap, int d
 
 // Capped scores in log2 units: y = s * P(s^2) while |s| * scale / cap <= 0.5,
 // with tanh(u) = u * (c0 + c1 u^2 + c2 u^4 + c3 u^6) to 5.7e-7 of it there, and
-// with u * (n0 + n1 u^2 + n2 u^4) to 4e-7 of it while it is at most 0.25. The
-// fits are minimax in the relative error: a fit of the absolute one is off by
-// 1.4e-6 to 2.3e-6 of a score far below the cap, which a row of few keys shows
-// in its log-sum.
+// (scored_attn alone) with u * (n0 + n1 u^2 + n2 u^4) to 4e-7 of it while it is
+// at most 0.25. The fits are minimax in the relative error: a fit of the
+// absolute one is off by 1.4e-6 to 2.3e-6 of a score far below the cap, which a
+// row of few keys shows in its log-sum.
 template <typename Args>
 void cap_coefficients(float scale, float softcap, Args* a) {
   constexpr const double (&kC)[4] = kTanhPoly;
@@ -167,7 +167,8 @@ void cap_coefficients(float scale, float softcap, Args* a) {
   bool finite = true;
   for (int i = 0; i < 4; ++i, f *= u * u) {
     a->cap_c[i] = static_cast<float>(kC[i] * f);
-    if (i < 3) a->cap_n[i] = static_cast<float>(kN[i] * f);
+    if constexpr (std::is_same<Args, ScoredArgs>::value)
+      if (i < 3) a->cap_n[i] = static_cast<float>(kN[i] * f);
     finite = finite && std::isfinite(a->cap_c[i]);
   }
   a->cap_in = u < 3e38 ? static_cast<float>(u) : 3e38f;
