@@ -161,3 +161,18 @@ def test_long_caches_whose_blocks_differ(d, N, Hq, Hkv, B, C, bias):
                            None if slopes is None else float(slopes[0]))
             with pytest.raises(AssertionError, match="O off"):
                 R.assert_attention(o[0, 0], lse[0, 0], ref)
+
+
+@pytest.mark.parametrize("softcap", [0.0, 30.0])
+def test_negative_slopes(softcap):
+    """Far keys come nearer: the row maxima rise along the walk, and rows beside their keys are moved as with others."""
+    g = gen(77)
+    slopes = torch.tensor([-0.05, -0.5, 0.25, -2.0 ** -9], device="cuda")
+    for Lq, Lk, start in ((700, 700, 0), (100, 1500, 700), (300, 400, 5000), (64, 900, -3000)):
+        check_scored(randn(g, 4, Lq, 64), randn(g, 2, Lk, 64), randn(g, 2, Lk, 64), softcap, slopes, q_start=start)
+    lo = torch.randint(0, 600, (700,), generator=g)
+    ranges = torch.stack([lo, lo + torch.randint(0, 300, (700,), generator=g)], 1).to(torch.int32).cuda()
+    check_scored(randn(g, 4, 700, 128), randn(g, 2, 700, 128), randn(g, 2, 700, 128), softcap, slopes, ranges)
+    c = random_cache(g, 2, 2, 4096, 128)
+    for B in (1, 24, 70):
+        check_cache_attn(randn(g, 2, 4, B, 128), c, [4000, 130], softcap, slopes, None if B == 1 else [9000, -50])
