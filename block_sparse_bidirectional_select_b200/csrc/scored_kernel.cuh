@@ -398,7 +398,6 @@ __global__ void __launch_bounds__(384, 1)
         return true;
       };
       int w = blockIdx.x;
-      bool skipped = false;  // the last pair had no second query tile
       while (ok) {
         if (w >= n_pairs) {
           publish(n_pairs, 0, 0, 0);
@@ -428,14 +427,6 @@ __global__ void __launch_bounds__(384, 1)
         // with a bias, the tile of the middle of the pair's rows
         const int near =
             BIAS ? min(max((a.q_start + pr.q0 * 128 + (pr.has1 ? 128 : 64)) / BK - j0, 0), max(nj - 1, 0)) : 0;
-        // Slot 1 waits for no tile of a pair without a query tile of its own. Before
-        // it takes part again all loads so far have landed, so that it can tell
-        // the phase of its next waits.
-        if (!split && pr.has1 && skipped) {
-          for (int u = seq > NST ? seq - NST : 0; ok && u < seq; ++u) ok = wait(C::B_FULL + u % NST, u / NST);
-          if (!ok) break;
-        }
-        skipped = !pr.has1;
         ok = publish(w, j0, nj, near);
         if (!ok) break;
         // the CTA's next turn: the static stride, or a claim on the counter
@@ -461,6 +452,11 @@ __global__ void __launch_bounds__(384, 1)
           if (ok && j == 0 && (split ? nj > 1 : pr.has1)) ok = load_q(1, split ? pr.q0 : pr.q0 + 1);
           if (ok) ok = load_tile(&tm_v, blk);
         }
+        // Slot 1 waits for no tile of a pair without a second query tile. All of
+        // them have landed before the next turn is published, so that slot 1 can
+        // tell the phase of its next waits.
+        if (!split && !pr.has1)
+          for (int u = seq > NST ? seq - NST : 0; ok && u < seq; ++u) ok = wait(C::B_FULL + u % NST, u / NST);
         w = w_next;
       }
       if (!ok) {

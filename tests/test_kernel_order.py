@@ -121,7 +121,7 @@ def test_cache_attention_epilogue_waits_for_the_tile_before_the_last():
                     r"\+ \(\(g - 1\) & 1\)\)", body[at:])
 
 
-# ------------------------------------------------------------------ ring stages of scored_attn
+# ------------------------------------------------------------------ ring stages of the two-tile kernels
 
 class RingWaiter:
     """What a warp knows about loads that complete in any order: those that it
@@ -139,39 +139,40 @@ class RingWaiter:
 
 
 def ring_waits(stages, split, turns, slot, lands=True):
-    """The loads that an issuer of scored_attn_kernel waits for: K_j is load
-    2 j, V_j load 2 j + 1. turns: (tiles, whether slot 1 has a query tile).
-    lands: the producer waits for its loads before a turn that slot 1 takes
-    part in again, and the issuer learns of the turn after that."""
-    w, seq, skipped = RingWaiter(stages), 0, False
+    """The loads that an issuer of scored_attn_kernel or attn_fwd_kernel waits
+    for: K_j is load 2 j, V_j load 2 j + 1. turns: (tiles, whether slot 1 has a
+    query tile). lands: after a turn without, the producer waits for its loads
+    before it publishes the next one, of which the issuers learn after that."""
+    w, seq = RingWaiter(stages), 0
     for tiles, has1 in turns:
-        if lands and not split and has1 and skipped:
-            w.waited.update(range(seq))
-            w.top = max(w.top, seq - 1)
-        skipped = not has1
         for j in range(tiles):
             if (j & 1) == slot if split else (slot == 0 or has1):
                 w.wait(seq)
                 w.wait(seq + 1)
             seq += 2
+        if lands and not split and not has1:
+            w.waited.update(range(seq))
+            w.top = max(w.top, seq - 1)
 
 
 TURNS = [[(n, b) for n in (1, 2, 3, 9)] + [(5, True), (7, False), (4, True)] for b in (False, True)]
 
 
-def test_scored_attention_waits_tell_their_phase(tmp_path):
+def test_ring_waits_tell_their_phase(tmp_path):
     """With the ring sizes of the build, compiled from its headers."""
     from block_sparse_bidirectional_select_b200.build import CSRC as csrc, nvcc_path
     src, exe = tmp_path / "ring.cu", tmp_path / "ring"
     src.write_text('#include <cstdio>\n#include "scored_kernel.cuh"\nusing namespace sparsed;\n'
-                   'int main() { std::printf("%d %d %d %d\\n", ScoredCfg<64>::NST, ScoredCfg<64>::NST_SPLIT, '
-                   'ScoredCfg<128>::NST, ScoredCfg<128>::NST_SPLIT); }\n')
+                   'int main() { std::printf("%d %d %d %d %d %d %d %d\\n", ScoredCfg<64>::NST, ScoredCfg<64>::NST_SPLIT, '
+                   'ScoredCfg<128>::NST, ScoredCfg<128>::NST_SPLIT, AttnCfg<64, 64>::NST, AttnCfg<64, 128>::NST, '
+                   'AttnCfg<128, 64>::NST, AttnCfg<128, 128>::NST); }\n')
     subprocess.run([nvcc_path(), "-gencode", "arch=compute_100a,code=sm_100a", "-std=c++17", "-I", csrc, "-o",
                     str(exe), str(src)], check=True)
     sizes = [int(x) for x in subprocess.run([str(exe)], check=True, capture_output=True, text=True).stdout.split()]
     for slot in (0, 1):
-        for ring, ring_split in (sizes[:2], sizes[2:]):
+        for ring, ring_split in (sizes[:2], sizes[2:4]):
             ring_waits(ring_split, True, [(40, False)], slot)
+        for ring in (sizes[0], sizes[2], *sizes[4:]):
             for turns in TURNS:
                 ring_waits(ring, False, turns, slot)
 
@@ -181,9 +182,9 @@ def test_the_ring_model_finds_the_unsafe_forms():
         ring_waits(5, True, [(8, False)], 0)
     with pytest.raises(AssertionError, match="may pass"):
         ring_waits(5, False, [(3, False), (3, True)], 1, lands=False)
-    # the split form has its own ring, and the producer waits ahead of the turn's publication
+    # the split form has its own ring, and the producers wait at the end of such a turn
     body = kernel_body(source("scored_kernel.cuh"), "scored_attn_kernel")
     assert "constexpr int NST = SPLIT ? S::NST_SPLIT : S::NST;" in body
-    wait = body.index("if (!split && pr.has1 && skipped) {")
-    assert body.index("wait(C::B_FULL + u % NST, u / NST)", wait) < body.index("skipped = !pr.has1;", wait) \
-        < body.index("ok = publish(w, j0, nj, near);", wait)
+    for text, given in ((body, "!split && !pr.has1"),):
+        assert re.search(r"ok = load_tile\(&tm_v, \w+\);\s*\}\s*if \(%s\)\s*for \(int u = seq > NST \? seq - NST : 0; ok && "
+                         r"u < seq; \+\+u\) ok = wait\(C::B_FULL \+ u %% NST, u / NST\);\s*w = w_next;" % re.escape(given), text)
