@@ -313,6 +313,11 @@ __global__ void __launch_bounds__(384, 1)
           if (ok && pr.has1 && j == 0) ok = load_q(1, pr.q0 + 1);
           if (ok) ok = load_tile(&tm_v, j);
         }
+        // Slot 1 waits for no tile of a pair without a second block. All of them
+        // have landed before the next pair is published, so that slot 1 can tell
+        // the phase of its next waits.
+        if (!pr.has1)
+          for (int u = seq > NST ? seq - NST : 0; ok && u < seq; ++u) ok = wait(C::B_FULL + u % NST, u / NST);
         w = w_next;
       }
       if (!ok) {

@@ -185,6 +185,7 @@ def test_the_ring_model_finds_the_unsafe_forms():
     # the split form has its own ring, and the producers wait at the end of such a turn
     body = kernel_body(source("scored_kernel.cuh"), "scored_attn_kernel")
     assert "constexpr int NST = SPLIT ? S::NST_SPLIT : S::NST;" in body
-    for text, given in ((body, "!split && !pr.has1"),):
+    for text, given in ((body, "!split && !pr.has1"),
+                        (kernel_body(source("attn_kernel.cuh"), "attn_fwd_kernel"), "!pr.has1")):
         assert re.search(r"ok = load_tile\(&tm_v, \w+\);\s*\}\s*if \(%s\)\s*for \(int u = seq > NST \? seq - NST : 0; ok && "
                          r"u < seq; \+\+u\) ok = wait\(C::B_FULL \+ u %% NST, u / NST\);\s*w = w_next;" % re.escape(given), text)
