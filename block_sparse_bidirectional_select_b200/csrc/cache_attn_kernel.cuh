@@ -60,11 +60,12 @@
 //   warps 12-15 widen V tiles (e4m3 -> f16, rows past the length cleared)
 // Every wait is bounded.
 //
-// Measured: 16 single tokens of 32 heads on 8 over 16384 keys (537 MB) 116 us,
-// 4.6 TB/s with set-up, joins and launches, 5.2 TB/s in the steady state; a
-// single token over 8192 keys 17 us, of which the tiles are 4; 64-token blocks of
-// 64 heads over 32768 keys with a bias 162 to 168 us. The single tokens are bound by
-// HBM, the blocks by the softmax chain of a tile.
+// Measured: 16 single tokens of 32 heads on 8 over 16384 keys (537 MB) 111 to
+// 116 us, 4.6 to 4.8 TB/s with set-up, joins and launches, 5.2 TB/s in the
+// steady state; a single token over 8192 keys 17 us, of which the tiles are 4;
+// two 64-token blocks of 32 heads over 32768 keys with a bias 162 to 170 us. No
+// unit is saturated (DRAM 44% busy for 4 single tokens, 29% for a block): what
+// bounds both is the chain of a tile, and the ends of the parts.
 #pragma once
 
 #include "cache_kernels.cuh"

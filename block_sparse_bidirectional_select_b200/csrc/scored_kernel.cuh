@@ -38,8 +38,8 @@
 // for those alone (kCapHigh). MUFU is what bounds that path (16 operations a
 // clock and SM, three per score with the softmax's own).
 //
-// Measured, 32 heads of 8192 tokens, d = 128: 1003 us plain (attn_fwd_kernel:
-// 995), 1010 with a bias, 1315 capped, 1505 capped and biased. What bounds them
+// Measured, 32 heads of 8192 tokens, d = 128: 1002 us plain (attn_fwd_kernel:
+// 995), 1010 to 1050 with a bias, 1300 capped, 1455 capped and biased. What bounds them
 // is a slot's chain (S and P share columns, so S waits for PV) and the power cap.
 #pragma once
 

@@ -627,10 +627,11 @@ int sparsed_cache_attn_workspace_bytes(int N, int Hq, int Hkv, int B, int d, siz
  *         (fp32 [N, Hq, B])
  * q_start (DEVICE [N] int32, null: lengths[n] - B; clamped to +-2^29) is the
  * position of a sequence's first query token. It may lie anywhere: a bias is
- * taken from the cached key nearest to it, and is right to 2^-22 of what it adds there. Cached bytes past lengths[n] are never used,
- * whatever they hold. length 0 gives O = 0 and LSE = -inf. LSE and O merge
+ * taken from the cached key nearest to it, and is right to 2^-22 of what it adds
+ * there. Cached bytes past lengths[n] are never used, whatever they hold. length 0 gives O = 0 and LSE = -inf. LSE and O merge
  * with attention over other keys by the two-part LSE identity. softcap >= 0,
- * scale >= 0, N <= 16384. Results do not depend on what else is in the batch up to
+ * scale >= 0, N <= 16384. V enters to 2^-24 of the largest V scale of its
+ * sequence and head. Results do not depend on what else is in the batch up to
  * rounding, and are the same bits on every call with the same lengths.
  * workspace: sparsed_cache_attn_workspace_bytes, 256-byte aligned, contents
  * ignored; one workspace must not serve two calls at the same time. */
@@ -662,9 +663,10 @@ int sparsed_scored_attn_workspace_bytes(int Hq, int Lq, size_t* bytes);
  *   x = x - slopes[h] * |q_start + r - c|   if slopes is given (DEVICE [Hq] fp32)
  *   O[h,r,:] = sum_c softmax(x)_c v_c  (bf16 [Hq, Lq, d]),
  *   LSE[h,r] = ln sum_c exp(x)         (fp32 [Hq, Lq])
- * A row that sees nothing gives O = 0 and LSE = -inf. What K and V hold at keys
- * that no row sees has no effect; a NaN or infinity in V at a key that some row
- * of the 256 rows 256 i .. 256 i + 255 of a head sees reaches all of those.
+ * Strides of dimensions above 1 are not 0. A row that sees nothing gives O = 0
+ * and LSE = -inf. What K and V hold at keys that no row sees has no effect; a
+ * NaN or infinity in V at a key that some row of the 256 rows 256 i ..
+ * 256 i + 255 of a head sees reaches all of those.
  * scale >= 0, softcap >= 0, |q_start| <= 2^29. A row may stand anywhere beside
  * its keys: a bias is taken from the visible key nearest to it, and is right to
  * 2^-22 of what it adds there.
