@@ -266,15 +266,15 @@ __device__ __forceinline__ ScoredPair scored_pair(const ScoredArgs& a, int w, in
 // The walk's j-th tile: from tile `near` down to the first, then on upwards.
 __device__ __forceinline__ int scored_tile(int j, int near) { return j <= near ? near - j : j; }
 
-// [lo, hi) of row r clamped to the keys; rows past the last see all of them
-// when `outside_all`, else nothing.
+// [lo, hi) of row r with 0 <= lo and 0 <= hi <= Lk, so that differences from key
+// positions fit; rows past the last see all keys when `outside_all`, else nothing.
 __device__ __forceinline__ int2 scored_range(const ScoredArgs& a, int r, bool outside_all) {
   int2 v = make_int2(0, a.Lk);
   if (r >= a.L) return outside_all ? v : make_int2(0, 0);
   if (a.ranges) {
     v = a.ranges[r];
     v.x = max(v.x, 0);
-    v.y = min(v.y, a.Lk);
+    v.y = min(max(v.y, 0), a.Lk);
   }
   return v;
 }

@@ -176,3 +176,17 @@ def test_negative_slopes(softcap):
     c = random_cache(g, 2, 2, 4096, 128)
     for B in (1, 24, 70):
         check_cache_attn(randn(g, 2, 4, B, 128), c, [4000, 130], softcap, slopes, None if B == 1 else [9000, -50])
+
+
+@pytest.mark.parametrize("H,softcap", [(2, 0.0), (40, 0.0), (40, 30.0)])
+def test_ranges_at_the_ends_of_their_type(H, softcap):
+    """Bounds next to -2^31 and 2^31 - 1, as rows of a tile that other rows do see."""
+    g = gen(78)
+    L, lowest, most = 600, -2 ** 31, 2 ** 31 - 1
+    q, k, v = randn(g, H, L, 64), randn(g, 2, L, 64), randn(g, 2, L, 64)
+    rows = [[0, lowest], [300, lowest], [0, lowest + 1], [lowest, most], [most, most], [most, lowest], [250, -1], [lowest, 400]]
+    ranges = torch.tensor([[0, L]] * L, dtype=torch.int32)
+    for i in range(L):
+        if i % 3:
+            ranges[i] = torch.tensor(rows[(i // 3) % len(rows)], dtype=torch.int32)
+    check_scored(q, k, v, softcap, None, ranges.cuda())
